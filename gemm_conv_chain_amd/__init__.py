@@ -11,16 +11,21 @@ The functions mirror the C entry points:
 * ``chain_conv_pool(x, w, b, act, pool)``      maxpool2x2(act(conv3x3(x) + b))
 * ``chain_conv2(x, w0, b0, w1, b1, act)``      conv1x1(act(conv3x3(x) + b0)) + b1
 * ``gemm_bias_act``, ``conv_bias_act``, ``maxpool2x2``   single operators
+* ``rope(x, positions, turns)``, ``kv_append(k, v, codes, ...)``,
+  ``chain_attn(q, codes, ...)``   rotary positions, appending to a paged cache of
+  8-bit codes (``kv_cache``), and attention over it (softmax(q K^T) V as a chain)
 * ``pad_channels`` / ``pad_weight_channels``   zero padding of channel counts
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 import re
 
-__all__ = ["TuneEntry", "tune_chain_gemm2_table", "auto_config", "tune_conv_pool", "conv_auto_config", "CONV_VARIANT", "lib", "FusedChainError", "chain_gemm2", "tune_chain_gemm2", "auto_variant", "tune_clear", "chain_gemmN", "chain_conv_pool", "chain_conv_bn_pool", "chain_conv2", "chain_convN", "convN_auto_variant", "tune_chain_convN",
+__all__ = ["DTYPE", "ATTN_VARIANT", "rope_turns", "rope", "kv_cache", "kv_append", "kv_check", "chain_attn", "attn_plan",
+           "TuneEntry", "tune_chain_gemm2_table", "auto_config", "tune_conv_pool", "conv_auto_config", "CONV_VARIANT", "lib", "FusedChainError", "chain_gemm2", "tune_chain_gemm2", "auto_variant", "tune_clear", "chain_gemmN", "chain_conv_pool", "chain_conv_bn_pool", "chain_conv2", "chain_convN", "convN_auto_variant", "tune_chain_convN",
            "gemm_bias_act", "conv_bias_act", "maxpool2x2", "avgpool2x2", "pad_channels", "pad_weight_channels", "abi_version", "ACT", "VARIANT",
            "LIB_PATH", "POISON_LIB_PATH", "poison_build", "HEADER_PATH", "exported_names"]
 
@@ -32,6 +37,8 @@ HEADER_PATH = os.path.join(os.path.dirname(_HERE), "include", "fusedchain.h")
 ACT = {"none": 0, "relu": 1, "gelu_tanh": 2, "hardswish": 3}
 POOL = {"none": 0, "max2x2": 1, "avg2x2": 2}
 VARIANT = {"auto": 0, "rf": 1, "lds": 2, "stream": 3, "pipe": 4}
+ATTN_VARIANT = {"auto": 0, "rows": 1, "tile": 2}
+DTYPE = {"float16": 0, "bfloat16": 1}
 CONV_VARIANT = {"auto": 0, "lds_weights": 1, "reg_weights": 2}
 
 
@@ -52,6 +59,28 @@ class TuneEntry(ctypes.Structure):
     launch."""
     _fields_ = [("variant", ctypes.c_int32), ("waves", ctypes.c_int32), ("stages", ctypes.c_int32),
                 ("us", ctypes.c_float)]
+
+
+class KvShape(ctypes.Structure):
+    """fc_kv_shape: the batch and the paged cache of kv_append and chain_attn."""
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "batch", "hq", "hkv", "d", "page", "pages", "table_stride")] + [
+        ("tokens", ctypes.c_int64), ("max_q", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
+
+
+class RopeTable(ctypes.Structure):
+    """fc_rope: turns a position of each pair (device), rotated elements, pairing, factor."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("mscale", ctypes.c_float)]
+
+
+class AttnParams(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("causal", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("variant", ctypes.c_int32), ("splits", ctypes.c_int32)]
+
+
+class AttnPlan(ctypes.Structure):
+    _fields_ = [("variant", ctypes.c_int32), ("splits", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("workspace", ctypes.c_int64)]
 
 
 _lib = None
@@ -152,9 +181,17 @@ def _load(path):
     L.winograd_weights.argtypes = [_vp, _vp, _i32, _i32, _vp]
     L.chain_conv_pool_winograd.argtypes = [_vp, _vp, _vp, ctypes.c_int, ctypes.c_int, _vp,
                                            ctypes.POINTER(ConvShape), _vp, _vp]
+    L.rope_apply.argtypes = [_vp, _vp, ctypes.POINTER(_i64), _vp, ctypes.POINTER(RopeTable), _i32, ctypes.c_int, _i64,
+                             _i32, _i32, _vp]
+    L.kv_append.argtypes = [_vp, _vp, _vp, _vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp,
+                            ctypes.POINTER(RopeTable), ctypes.POINTER(KvShape), _vp]
+    L.chain_attn_plan.argtypes = [ctypes.POINTER(KvShape), ctypes.POINTER(AttnParams), ctypes.POINTER(AttnPlan)]
+    L.chain_attn.argtypes = [_vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnParams), _vp,
+                             _vp, ctypes.POINTER(KvShape), _vp, _i64, _vp]
+    L.kv_check.argtypes = [_vp, _vp, _vp, ctypes.POINTER(KvShape), _i32]
     L.fc_tune_clear.restype = None
     L.fc_tune_clear.argtypes = []
-    for name in ("chain_conv2_auto_config", "chain_conv2_ex", "chain_conv2_variant", "chain_conv2_tune", "winograd_weights", "chain_conv_pool_winograd", "chain_gemm2_ex", "chain_gemm2_tune_ex", "chain_gemm2_auto_config", "chain_conv_pool_tune",
+    for name in ("rope_apply", "kv_append", "chain_attn_plan", "chain_attn", "kv_check", "chain_conv2_auto_config", "chain_conv2_ex", "chain_conv2_variant", "chain_conv2_tune", "winograd_weights", "chain_conv_pool_winograd", "chain_gemm2_ex", "chain_gemm2_tune_ex", "chain_gemm2_auto_config", "chain_conv_pool_tune",
                  "chain_conv_pool_auto_config", "chain_conv_pool_ex", "avgpool2x2", "fc_probe_mfma", "fc_probe_read", "chain_conv_bn_pool", "chain_convN", "chain_convN_variant", "chain_convN_auto_variant", "chain_convN_tune", "chain_gemm2_tune", "chain_gemm2_auto_variant", "chain_gemm2", "chain_gemm2_variant", "chain_gemmN", "chain_conv_pool", "chain_conv2", "gemm_bias_act",
                  "conv_bias_act", "maxpool2x2", "pad_channels"):
         getattr(L, name).restype = ctypes.c_int
@@ -745,3 +782,292 @@ def pad_weight_channels(w, c_out):
     out = _torch().empty((r, s, c_out, k), dtype=w.dtype, device=w.device)
     _check("pad_channels", lib().pad_channels(_ptr(w), _ptr(out), r * s, c_in, c_out, k, _stream(w)))
     return out
+
+
+# ---------------------------------------- attention over a paged 8-bit cache
+_STRIDES = {n: _i64 * n for n in (2, 4, 6)}
+
+
+def _rows(t, name, dtype=None):
+    """t [tokens, heads, d] of a 16-bit float type, elements of a head adjacent;
+    token and head strides are free.  Returns its fc_dtype."""
+    torch = _torch()
+    if len(_ndim(t, name, 3)) != 3:
+        raise ValueError("%s must be [tokens, heads, d]" % name)
+    if t.dtype is torch.float16:
+        code = 0
+    elif t.dtype is torch.bfloat16:
+        code = 1
+    else:
+        raise TypeError("%s must be torch.float16 or torch.bfloat16, got %s" % (name, t.dtype))
+    if dtype is not None and code != dtype:
+        raise TypeError("%s is %s, unlike the other activations" % (name, t.dtype))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError("the elements of a head of %s must be adjacent" % name)
+    return code
+
+
+def _same_device(items):
+    dev = None
+    for t, name in items:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TypeError("%s must be a device tensor" % name)
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
+
+
+def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=4.0, device=None):
+    """(turns, mscale) of a rotary table: turns int64 [rot / 2], pair i's turns a
+    position as 64-bit fractions (2^64 = one turn).  Without scaling pair i's
+    frequency is f_i = base^(-2 i / rot) radians a position.  scaling, for
+    contexts ``factor`` times as long as trained on:
+
+    * "linear"       f_i / factor;
+    * "base"         base raised to base * factor^(rot / (rot - 2)), which leaves the
+                     first pair as it is and stretches the last by factor;
+    * "wavelength"   pairs that turn at least ``high`` times within ``original``
+                     positions stay, those that turn at most ``low`` times are
+                     divided by factor, those between blend linearly in their
+                     number of turns;
+    * "ramp"         the same with the blend linear in the pair's index (between
+                     the indices where ``high``, 32 by custom, and ``low`` turns
+                     are reached), and mscale = 0.1 ln(factor) + 1.
+    """
+    torch = _torch()
+    if rot <= 0 or rot % 16:
+        raise ValueError("rot must be a positive multiple of 16, got %r" % (rot,))
+    if not base > 1.0 or not factor >= 1.0:
+        raise ValueError("base > 1 and factor >= 1 required")
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    mscale = 1.0
+    if scaling == "base":
+        base = base * factor ** (rot / (rot - 2))
+    f = base ** (-2.0 * i / rot)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("wavelength", "ramp"):
+        if not original or original <= 0 or not high > low:
+            raise ValueError("scaling %r needs original > 0 and high > low" % scaling)
+        if scaling == "wavelength":
+            keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        else:
+            def index(turns):
+                return rot * math.log(original / (turns * 2 * math.pi)) / (2 * math.log(base))
+            first = max(math.floor(index(high)), 0)
+            last = min(math.ceil(index(low)), rot - 1)
+            keep = 1.0 - ((i - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
+            mscale = 0.1 * math.log(factor) + 1.0
+        f = f * keep + f / factor * (1.0 - keep)
+    elif scaling not in (None, "base"):
+        raise ValueError("unknown scaling %r" % (scaling,))
+    turns = torch.round(f / (2 * math.pi) * 2.0 ** 64).to(torch.int64)
+    return (turns if device is None else turns.to(device)), mscale
+
+
+def _table(turns, interleaved, mscale):
+    torch = _torch()
+    if turns is None:
+        return None
+    _ndim(turns, "turns", 1)
+    if turns.dtype is not torch.int64:
+        raise TypeError("turns must be torch.int64, got %s" % turns.dtype)
+    if not turns.is_contiguous():
+        raise ValueError("turns must be contiguous")
+    return RopeTable(turns.data_ptr(), 2 * turns.shape[0], 1 if interleaved else 0, mscale)
+
+
+def rope(x, positions, turns, interleaved=False, mscale=1.0, inverse=False, out=None):
+    """x [tokens, heads, d] with the first 2 * len(turns) elements of each head
+    turned by its token's position (``positions`` int32 [tokens]): the pairs (i, i +
+    rot / 2), or (2 i, 2 i + 1) if ``interleaved``.  ``inverse`` turns back, which is
+    also the gradient.  ``out`` may be x itself."""
+    dt = _rows(x, "x")
+    T, H, D = x.shape
+    table = _table(turns, interleaved, mscale)
+    if table is None:
+        raise ValueError("turns is required")
+    _ndim(positions, "positions", 1)
+    if positions.dtype is not _torch().int32:
+        raise TypeError("positions must be torch.int32, got %s" % positions.dtype)
+    if positions.shape[0] != T or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous with shape (%d,), got %s" % (T, tuple(positions.shape)))
+    if out is None:
+        _same_device(((x, "x"), (positions, "positions"), (turns, "turns")))
+        out = _empty((T, H, D), x)
+    else:
+        if _rows(out, "out", dt) is not None and tuple(out.shape) != (T, H, D):
+            raise ValueError("out must have shape %s, got %s" % ((T, H, D), tuple(out.shape)))
+        _same_device(((x, "x"), (positions, "positions"), (turns, "turns"), (out, "out")))
+    st = _STRIDES[4](x.stride(0), x.stride(1), out.stride(0), out.stride(1))
+    _check("rope", lib().rope_apply(_ptr(x), _ptr(out), st, _ptr(positions), table, 1 if inverse else 0, dt, T, H, D,
+                                    _stream(x)))
+    return out
+
+
+def kv_cache(pages, hkv, page, d, device="cuda"):
+    """An empty pool: (codes uint8 [pages, hkv, 2, page / 16, 16 d], scales float32
+    [pages, hkv, 2]).  Its pages need no clearing between sequences."""
+    torch = _torch()
+    if page % 16:
+        raise ValueError("page must be a multiple of 16, got %d" % page)
+    return (torch.zeros((pages, hkv, 2, page // 16, 16 * d), dtype=torch.uint8, device=device),
+            torch.ones((pages, hkv, 2), dtype=torch.float32, device=device))
+
+
+def _kv_shape(dt, tokens, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv):
+    """Checks the cache's and the batch's tensors against each other."""
+    torch = _torch()
+    P, H, two, n, w = _ndim(codes, "codes", 5)
+    if (H, two, w) != (hkv, 2, 16 * d):
+        raise ValueError("codes must have shape (pages, %d, 2, page / 16, %d), got %s" % (hkv, 16 * d, tuple(codes.shape)))
+    B, stride = _ndim(table, "table", 2)
+    for t, name, shape, dtype in ((codes, "codes", None, torch.uint8), (scales, "scales", (P, H, 2), torch.float32),
+                                  (table, "table", None, torch.int32), (cu_q, "cu_q", (B + 1,), torch.int32),
+                                  (kv_lens, "kv_lens", (B,), torch.int32)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch tensor, got %s" % (name, type(t).__name__))
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        if shape is not None and tuple(t.shape) != shape:
+            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
+        if not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+    page = 16 * n
+    return KvShape(dt, B, hq, hkv, d, page, P, stride, tokens, tokens if max_q is None else int(max_q),
+                   min(stride * page, 0x7fffffff) if max_kv is None else int(max_kv))
+
+
+def kv_append(k, v, codes, scales, table, cu_q, kv_lens, turns=None, interleaved=False, mscale=1.0, positions=None,
+              q=None, q_out=None, max_q=None):
+    """Append k, v [tokens, hkv, d] to the paged cache (codes, scales), k turned by
+    the rotary table ``turns`` on the way (None: as it is).  Sequence b's new tokens
+    are rows cu_q[b]:cu_q[b+1] and the last of its kv_lens[b] tokens; slot s is in
+    page table[b, s // page].  ``positions`` (int32 [tokens]) turn instead of the slots.
+    With ``q`` [tokens, hq, d] the same launch returns q turned alike (``q_out``).
+    ``max_q``: a bound of the new tokens of a sequence; it sizes the launch."""
+    dt = _rows(k, "k")
+    _rows(v, "v", dt)
+    T, hkv, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape %s, got %s" % (tuple(k.shape), tuple(v.shape)))
+    hq = hkv
+    if q is not None:
+        _rows(q, "q", dt)
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q must have shape (%d, hq, %d), got %s" % (T, d, tuple(q.shape)))
+        hq = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, None)
+    rt = _table(turns, interleaved, mscale)
+    if positions is not None:
+        _ndim(positions, "positions", 1)
+        if positions.dtype is not _torch().int32:
+            raise TypeError("positions must be torch.int32, got %s" % positions.dtype)
+        if positions.shape[0] != T or not positions.is_contiguous():
+            raise ValueError("positions must be contiguous with shape (%d,), got %s" % (T, tuple(positions.shape)))
+    if q_out is not None:
+        _rows(q_out, "q_out", dt)
+        if q_out.shape != q.shape or not q_out.is_contiguous():
+            raise ValueError("q_out must be contiguous with shape %s, got %s" % (tuple(q.shape), tuple(q_out.shape)))
+    _same_device(((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (codes, "codes"), (scales, "scales"),
+                  (table, "table"), (cu_q, "cu_q"), (kv_lens, "kv_lens"), (positions, "positions"), (turns, "turns")))
+    if q is not None and q_out is None:
+        q_out = _empty((T, hq, d), q)
+    qs = (0, 0) if q is None else (q.stride(0), q.stride(1))
+    st = _STRIDES[6](k.stride(0), k.stride(1), v.stride(0), v.stride(1), *qs)
+    _check("kv_append", lib().kv_append(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), st, _ptr(codes), _ptr(scales),
+                                        _ptr(table), _ptr(cu_q), _ptr(kv_lens), _ptr(positions), rt, sh, _stream(k)))
+    return q_out
+
+
+def kv_check(table, cu_q, kv_lens, pages, page, tokens=None, writes=False):
+    """Look HOST copies (int32 tensors) of a batch's table, cu_q and kv_lens over:
+    raises FusedChainError at the first fault (an id outside the pool, a length the
+    table cannot hold, ...; with ``writes`` also a page to be written that two
+    sequences name).  On the device such faults give NaN rows."""
+    torch = _torch()
+    B, stride = _ndim(table, "table", 2)
+    for t, name, shape in ((table, "table", (B, stride)), (cu_q, "cu_q", (B + 1,)), (kv_lens, "kv_lens", (B,))):
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.is_cuda:
+            raise TypeError("%s must be a host tensor of torch.int32" % name)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError("%s must be contiguous with shape %s, got %s" % (name, shape, tuple(t.shape)))
+    n = int(cu_q[-1]) if tokens is None else int(tokens)
+    sh = KvShape(0, B, 1, 1, 64, int(page), int(pages), stride, max(n, 0), 0, 0)
+    _check("kv_check", lib().kv_check(_ptr(table), _ptr(cu_q), _ptr(kv_lens), sh, 1 if writes else 0))
+
+
+def _attn_params(d, scale, causal, softcap, window, variant, splits):
+    v = ATTN_VARIANT[variant] if isinstance(variant, str) else int(variant)
+    return AttnParams(d ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, int(window), v, int(splits))
+
+
+_ATTN_VARIANT_NAME = {v: k for k, v in ATTN_VARIANT.items()}
+
+
+def attn_plan(tokens, batch, hq, hkv, d, page, table_stride, max_q, max_kv, dtype="bfloat16", causal=True, window=0,
+              variant="auto", splits=0):
+    """{variant, splits, chunk, workspace}: the kernel form chain_attn runs, the blocks
+    a sequence's keys are split over, keys a block, workspace bytes (host only)."""
+    sh = KvShape(DTYPE[dtype], batch, hq, hkv, d, page, 1, table_stride, tokens, max_q, max_kv)
+    plan = AttnPlan()
+    _check("chain_attn_plan", lib().chain_attn_plan(sh, _attn_params(d, None, causal, 0.0, window, variant, splits), plan))
+    return {"variant": _ATTN_VARIANT_NAME[plan.variant], "splits": int(plan.splits), "chunk": int(plan.chunk),
+            "workspace": int(plan.workspace)}
+
+
+def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, softcap=0.0, window=0, slopes=None,
+               max_q=None, max_kv=None, out=None, lse=None, workspace=None, variant="auto", splits=0):
+    """out [tokens, hq, d] = softmax(scale * q K^T) V over the paged cache: queries
+    cu_q[b]:cu_q[b+1] are the last of sequence b's kv_lens[b] tokens and, if ``causal``,
+    see the slots up to their own (the last ``window`` of them if window > 0).
+    ``scale``: 1 / sqrt(d) by default; ``softcap`` > 0: scores become softcap *
+    tanh(score / softcap); ``slopes`` (float32 [hq]): minus slope * distance.  A row that
+    sees no key is 0.  ``lse``: None, True (allocate) or a float32 [tokens, hq] tensor;
+    returns out or (out, lse).  ``max_q``, ``max_kv``: bounds of the new tokens and lengths
+    (they size the launch); ``workspace``: uint8 device memory of attn_plan's size
+    (allocated if None); ``variant``, ``splits``: kernel form and split, by rule if not given."""
+    torch = _torch()
+    dt = _rows(q, "q")
+    T, hq, d = q.shape
+    hkv = codes.shape[1] if _ndim(codes, "codes", 5) else 0
+    sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv)
+    pa = _attn_params(d, scale, causal, softcap, window, variant, splits)
+    if slopes is not None and (_ndim(slopes, "slopes", 1) != (hq,) or not slopes.is_contiguous()):
+        raise ValueError("slopes must be contiguous with shape (%d,), got %s" % (hq, tuple(slopes.shape)))
+    if slopes is not None and slopes.dtype is not torch.float32:
+        raise TypeError("slopes must be torch.float32, got %s" % slopes.dtype)
+    if out is not None:
+        _rows(out, "out", dt)
+        if out.shape != q.shape or not out.is_contiguous():
+            raise ValueError("out must be contiguous with shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+    le = None if lse is True or lse is False else lse
+    if le is not None:
+        _ndim(le, "lse", 2)
+        if le.dtype is not torch.float32:
+            raise TypeError("lse must be torch.float32, got %s" % le.dtype)
+        if tuple(le.shape) != (T, hq) or not le.is_contiguous():
+            raise ValueError("lse must be contiguous with shape %s, got %s" % ((T, hq), tuple(le.shape)))
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
+        raise TypeError("workspace must be contiguous torch.uint8")
+    _same_device(((q, "q"), (codes, "codes"), (scales, "scales"), (table, "table"), (cu_q, "cu_q"),
+                  (kv_lens, "kv_lens"), (slopes, "slopes"), (out, "out"), (le, "lse"), (workspace, "workspace")))
+    L = lib()
+    plan = AttnPlan()
+    _check("chain_attn", L.chain_attn_plan(sh, pa, plan))
+    if out is None:
+        out = _empty((T, hq, d), q)
+    if lse is True:
+        le = _empty((T, hq), q, torch.float32)
+    if workspace is None and plan.workspace:
+        workspace = torch.empty(plan.workspace, dtype=torch.uint8, device=q.device)
+    st = _STRIDES[2](q.stride(0), q.stride(1))
+    _check("chain_attn", L.chain_attn(_ptr(q), st, _ptr(codes), _ptr(scales), _ptr(table), _ptr(cu_q), _ptr(kv_lens),
+                                      _ptr(slopes), pa, _ptr(out), _ptr(le), sh, _ptr(workspace),
+                                      0 if workspace is None else workspace.numel(), _stream(q)))
+    return (out, le) if le is not None else out

@@ -61,6 +61,13 @@ fc_status ok()
     return FC_OK;
 }
 
+}  // namespace
+namespace fc {
+// The detail message for entry points in other files: records it, returns s.
+int api_fail(int s, const char* msg) { return s == FC_OK ? ok() : fail((fc_status)s, "%s", msg); }
+}  // namespace fc
+namespace {
+
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
 fc_status hip_status(hipError_t e, const char* what)

@@ -29,6 +29,7 @@ inline hipError_t allow_full_lds(const void* f, std::atomic<unsigned long long>*
 }
 
 int device_cu_count();
+int api_fail(int status, const char* msg);   // sets the calling thread's fc_last_error, returns status
 bool rf_fits(int K0, int N0, int N1);
 bool stream_fits(int N0, int N1);
 bool gemmn_fits(int nst, const int* widths);

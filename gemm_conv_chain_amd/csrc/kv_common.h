@@ -1,0 +1,296 @@
+// kv_common.h -- what the attention-serving kernels (rope.hip, kv_append.hip,
+// attn_rows.hip, attn_tile.hip) share: the activations' types, the cache's
+// layout, the lookup of a page and the angle of a position.
+//
+// Layout of the cache.  codes [pages][kv heads][2 (K, V)][page / 16][16 * d],
+// OCP e4m3 bytes, in blocks of 16 tokens that are the matrix instructions' own
+// operand order, so that a fragment is loaded by 16 bytes a lane from
+// consecutive addresses, with no transposition on the way:
+//     K block  [d / 16][16 tokens][16 dims]     (operand A of K q: rows = keys)
+//     V block  [d][16 tokens]                   (operand A of V^T p: rows = dims)
+// scales [pages][kv heads][2]: a power of two for each page, head and side.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fc_device.h"
+
+namespace fc {
+
+typedef __bf16 bf16_t;
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+
+enum { DT_F16 = 0, DT_BF16 = 1 };
+
+// Strides in elements; see fc_kv_shape.
+struct KvShape {
+    int batch, hq, hkv, d, page, pages, table_stride;
+    long tokens;
+    int max_q, max_kv;
+};
+
+struct RopeArgs {
+    const unsigned long long* turns;   // [rot / 2], fractions of a turn a position, 2^64 = one turn
+    int rot, interleaved;
+    float mscale;
+};
+
+// Type traits: vectors of 8, conversions, the two matrix instructions.
+template <class T> struct Tr;
+template <> struct Tr<half_t> {
+    typedef half8 v8;
+    static constexpr int elo = -15, ehi = 7;    // scale exponents: code * scale is exactly an fp16 value
+    __device__ static __forceinline__ unsigned from_fp8(unsigned w, float s, bool hi)
+    {
+        return hi ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true))
+                  : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, false));
+    }
+    __device__ static __forceinline__ unsigned pk(float a, float b)
+    {
+        half2v h;
+        h[0] = (half_t)a;
+        h[1] = (half_t)b;
+        return __builtin_bit_cast(unsigned, h);
+    }
+    __device__ static __forceinline__ floatx4 mfma16(v8 a, v8 b, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+    }
+    __device__ static __forceinline__ floatx16 mfma32(v8 a, v8 b, floatx16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+template <> struct Tr<bf16_t> {
+    typedef bf8 v8;
+    static constexpr int elo = -100, ehi = 119;
+    __device__ static __forceinline__ unsigned from_fp8(unsigned w, float s, bool hi)
+    {
+        return hi ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))
+                  : __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, false));
+    }
+    __device__ static __forceinline__ unsigned pk(float a, float b)
+    {
+        bf2 h;
+        h[0] = (bf16_t)a;
+        h[1] = (bf16_t)b;
+        return __builtin_bit_cast(unsigned, h);
+    }
+    __device__ static __forceinline__ floatx4 mfma16(v8 a, v8 b, floatx4 c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+    }
+    __device__ static __forceinline__ floatx16 mfma32(v8 a, v8 b, floatx16 c)
+    {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+
+// 8 codes (two dwords) to a matrix operand of 8 values, times the power of two s.
+template <class T>
+__device__ __forceinline__ typename Tr<T>::v8 frag8(unsigned w0, unsigned w1, float s)
+{
+    u32x4 r;
+    r[0] = Tr<T>::from_fp8(w0, s, false);
+    r[1] = Tr<T>::from_fp8(w0, s, true);
+    r[2] = Tr<T>::from_fp8(w1, s, false);
+    r[3] = Tr<T>::from_fp8(w1, s, true);
+    return __builtin_bit_cast(typename Tr<T>::v8, r);
+}
+
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8])
+{
+    const typename Tr<T>::v8 v = *reinterpret_cast<const typename Tr<T>::v8*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
+}
+
+template <class T>
+__device__ __forceinline__ u32x4 pack8(const float (&x)[8])
+{
+    u32x4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = Tr<T>::pk(x[2 * i], x[2 * i + 1]);
+    return r;
+}
+
+// The byte of the pool at which (page id, head, side) begins.
+__device__ __forceinline__ size_t side_base(int id, int h, int side, const KvShape& s)
+{
+    return ((size_t)((size_t)id * s.hkv + h) * 2 + side) * ((size_t)s.page * s.d);
+}
+
+// The id of page `pidx` of sequence b, or -1 where the table has none: an index
+// past the table's row or an id outside the pool.  Every kernel goes through
+// this, so that no table can make it read or write outside the pool.
+__device__ __forceinline__ int page_id(const int* table, const KvShape& s, int b, int pidx)
+{
+    if ((unsigned)pidx >= (unsigned)s.table_stride) return -1;
+    const int id = table[(size_t)b * s.table_stride + pidx];
+    return (unsigned)id < (unsigned)s.pages ? id : -1;
+}
+
+// Sequence b's first token and its number of new tokens, inside [0, tokens).
+__device__ __forceinline__ void seq_range(const int* cu_q, const KvShape& s, int b, long* first, int* n)
+{
+    long a = cu_q[b], z = cu_q[b + 1];
+    a = a < 0 ? 0 : (a > s.tokens ? s.tokens : a);
+    z = z < a ? a : (z > s.tokens ? s.tokens : z);
+    *first = a;
+    *n = (int)(z - a);
+}
+
+// Sequence b's number of keys.  A length that its row of the table cannot hold
+// counts as none, and *over makes the caller's results NaN: a broken length
+// neither reads past the table nor keeps a kernel busy.
+__device__ __forceinline__ int seq_keys(const int* kv_lens, const KvShape& s, int b, bool* over)
+{
+    const int n = kv_lens[b];
+    *over = n > s.page * s.table_stride;
+    return n < 0 || *over ? 0 : n;
+}
+
+// sin and cos of position p times the frequency f (a 64-bit fraction of a
+// turn).  The product's low 64 bits are the turn's fraction, exact for every
+// 32-bit position (the far ones too, where a 32-bit float angle is off by
+// whole radians); its upper 32 bits go to the hardware's sine and cosine,
+// which take turns.  Measured against 64 bits over the turn: 1.25e-7 absolute.
+__device__ __forceinline__ void turn_sincos(int p, unsigned long long f, float& sn, float& cs)
+{
+    const unsigned lo = (unsigned)f, hi = (unsigned)(f >> 32), u = (unsigned)p;
+    unsigned frac = __umulhi(u, lo) + u * hi;
+    if (p < 0) frac -= lo;   // u = p + 2^32
+    const float t = (float)(int)frac * 0x1p-32f;
+    sn = __builtin_amdgcn_sinf(t);
+    cs = __builtin_amdgcn_cosf(t);
+}
+
+// One unit of 16 elements of a head: 8 rotated pairs, or 16 elements that pass.
+// Unit u < rot / 16 holds the pairs 8u .. 8u + 7; the elements sit at e0 .. e0
+// + 7 and e1 .. e1 + 7.
+struct Unit {
+    int e0, e1;
+    bool turned;
+};
+__device__ __forceinline__ Unit unit_of(int u, int rot, int interleaved)
+{
+    Unit r;
+    r.turned = u * 16 < rot;
+    const bool half = r.turned && !interleaved;
+    r.e0 = half ? u * 8 : u * 16;
+    r.e1 = half ? rot / 2 + u * 8 : u * 16 + 8;
+    return r;
+}
+
+// x0, x1: the elements at e0.. and e1..; cs, sn: the 8 pairs' cosines and sines.
+__device__ __forceinline__ void rotate_unit(float (&x0)[8], float (&x1)[8], const float (&cs)[8], const float (&sn)[8],
+                                            int interleaved)
+{
+    if (!interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = x0[j], b = x1[j];
+            x0[j] = a * cs[j] - b * sn[j];
+            x1[j] = a * sn[j] + b * cs[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = x0[2 * j], b = x0[2 * j + 1], c = x1[2 * j], d = x1[2 * j + 1];
+            x0[2 * j] = a * cs[j] - b * sn[j];
+            x0[2 * j + 1] = a * sn[j] + b * cs[j];
+            x1[2 * j] = c * cs[4 + j] - d * sn[4 + j];
+            x1[2 * j + 1] = c * sn[4 + j] + d * cs[4 + j];
+        }
+    }
+}
+
+__device__ __forceinline__ void unit_angles(const unsigned long long* turns, int u, int p, float mscale, float sign,
+                                            float (&cs)[8], float (&sn)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        turn_sincos(p, turns[u * 8 + j], sn[j], cs[j]);
+        cs[j] *= mscale;
+        sn[j] *= mscale * sign;
+    }
+}
+
+// Maximum over the lanes l, l ^ 32 (and l ^ 16): a register swap with itself
+// puts the two halves (rows of 16) side by side.
+__device__ __forceinline__ float max_x32(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__builtin_bit_cast(float, (unsigned)p[0]), __builtin_bit_cast(float, (unsigned)p[1]));
+}
+__device__ __forceinline__ float max_x16(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return fmaxf(__builtin_bit_cast(float, (unsigned)p[0]), __builtin_bit_cast(float, (unsigned)p[1]));
+}
+__device__ __forceinline__ float sum_x32(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __builtin_bit_cast(float, (unsigned)p[0]) + __builtin_bit_cast(float, (unsigned)p[1]);
+}
+__device__ __forceinline__ float sum_x16(float v)
+{
+    const unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return __builtin_bit_cast(float, (unsigned)p[0]) + __builtin_bit_cast(float, (unsigned)p[1]);
+}
+
+// The attention kernels' arguments.  A "row" is one query of one head; rows of
+// the heads that share a kv head are adjacent: row r of (sequence, kv head) is
+// query r / G, head h * G + r % G.
+struct AttnArgs {
+    const void* q;
+    long q_ts, q_hs;
+    const uint8_t* codes;
+    const float* scales;
+    const int *table, *cu_q, *kv_lens;
+    const float* slopes;   // [hq] or NULL
+    void* out;             // [tokens, hq, d]
+    float* lse;            // [tokens, hq] or NULL
+    float *part_o, *part_ml;   // workspace of nsplit > 1: [tokens, hq, nsplit, d] and [.., 2]
+    KvShape s;
+    int G, causal, window, nsplit, chunk;   // chunk: blocks of 16 keys a split
+    float scale, cap;
+    FastDiv by_g;
+};
+
+// The keys that rows r0 .. r1 - 1 (of q_len * G) may see, as blocks of 16
+// [*g0, *g1), and the first query's position.
+__device__ __forceinline__ void key_range(const AttnArgs& a, int kv_len, int pos0, int t0, int t1, int* g0, int* g1)
+{
+    int lo = a.window > 0 ? pos0 + t0 - a.window + 1 : 0;
+    int hi = a.causal ? pos0 + t1 + 1 : kv_len;   // t1: the last query
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > kv_len ? kv_len : hi;
+    *g0 = lo >> 4;
+    *g1 = hi > lo ? (hi + 15) >> 4 : *g0;
+}
+
+// Score modification, in units of log 2: s is q . k on the codes.  Without a
+// cap c0 = k scale * softmax scale * log2 e; with one c0 = 2 log2 e * k scale *
+// softmax scale / cap and c1 = cap * log2 e: cap tanh(x) = cap (1 - 2 / (1 +
+// e^2x)), whose absolute error of 1e-7 cap is far under what 16-bit queries
+// carry, and which saturates at both ends.
+template <bool CAP>
+__device__ __forceinline__ float score(float s, float c0, float c1)
+{
+    if (!CAP) return s * c0;
+    return c1 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * c0)));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+
+}  // namespace fc

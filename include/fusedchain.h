@@ -493,6 +493,143 @@ fc_status winograd_weights(const fc_half *w, fc_half *U, int32_t c, int32_t k, v
 fc_status chain_conv_pool_winograd(const fc_half *x, const fc_half *U, const fc_half *b, fc_act act, fc_pool pool,
                                    fc_half *y, const fc_conv_shape *shape, uint8_t *argmax, void *stream);
 
+/* ---- attention over a paged 8-bit cache: the chain q K^T -> softmax -> V -----
+ *
+ * The same chain as above (two products, an element-wise step between them, the
+ * intermediate on chip), for the attention layer of a decoder that serves many
+ * sequences: rope_apply turns queries and keys by their positions, kv_append
+ * writes keys and values into a paged cache of 8-bit codes, chain_attn reads
+ * it.  These entry points were added under ABI version 4; nothing that version
+ * had has changed.
+ *
+ * Types: activations are FC_F16 or FC_BF16 (all of one call alike); codes are
+ * OCP e4m3; scales, slopes and lse are fp32; indices, lengths and positions
+ * int32 in device memory.
+ *
+ * Ragged batch: sequence b's new tokens are rows cu_q[b] .. cu_q[b+1] - 1 of q,
+ * k and v, and the last of its kv_lens[b] tokens (the length AFTER the append):
+ * the i-th of its n new tokens sits at slot kv_lens[b] - n + i.  n may be 0.
+ *
+ * Cache: codes [pages][hkv][2][page/16][16*d] bytes (side 0 = K, 1 = V); a
+ * block of 16 tokens is [d/16][16 tokens][16 dims] for K and [d][16 tokens] for
+ * V, the matrix cores' operand order.  scales [pages][hkv][2], powers of two:
+ * a value is code * scale.  Slot s of sequence b is token s % page of page
+ * table[b][s / page]; table is [batch][table_stride].  A page may be read by
+ * several sequences (a shared prefix) but written by one only.
+ *
+ * Bad metadata cannot make a kernel leave its buffers: page ids outside the
+ * pool, or lengths that the table's row cannot hold, make the rows of out (and
+ * lse) that would read them NaN, and such tokens are not appended; cu_q is
+ * taken inside [0, tokens].  kv_check finds such faults on host copies.
+ */
+typedef enum { FC_F16 = 0, FC_BF16 = 1 } fc_dtype;
+
+typedef struct {
+    int32_t dtype;          /* fc_dtype */
+    int32_t batch;          /* sequences */
+    int32_t hq, hkv;        /* query heads, kv heads; hq % hkv == 0, query head i reads kv head i / (hq / hkv) */
+    int32_t d;              /* head size: 64, 128, 192 or 256 */
+    int32_t page;           /* tokens a page: 16, 32, 64, 128 or 256 */
+    int32_t pages;          /* pages of the pool */
+    int32_t table_stride;   /* entries of a sequence's row of the table */
+    int64_t tokens;         /* rows of q, k, v */
+    int32_t max_q;          /* the largest number of new tokens of a sequence, and                */
+    int32_t max_kv;         /* the largest length: they size the launch; wrong values cost time only */
+} fc_kv_shape;
+
+/* A rotary table: turns [rot/2] (device), the pair's turns a position as
+ * 64-bit fractions (2^64 = one turn; frequency f radians a position is
+ * round(f / (2 pi) * 2^64)), so that an angle is exact at every 32-bit
+ * position.  The first rot (a multiple of 16, <= d) elements of a head turn:
+ * element i with i + rot/2, or 2i with 2i + 1 if interleaved.  mscale
+ * multiplies both results. */
+typedef struct {
+    const int64_t *turns;
+    int32_t rot, interleaved;
+    float mscale;
+} fc_rope;
+
+/*
+ * rope_apply -- y = x with each pair (a, b) of the rotary part turned by its
+ * token's position: mscale * (a cos - b sin, a sin + b cos); inverse != 0 turns
+ * the other way (the gradient).  x, y [tokens, heads, d], strides in elements
+ * {x token, x head, y token, y head}, multiples of 8; positions [tokens], any
+ * int32.  d % 16 == 0, d <= 1024.  y may be x (with x's strides).
+ */
+fc_status rope_apply(const void *x, void *y, const int64_t *strides, const int32_t *positions, const fc_rope *rope,
+                     int32_t inverse, fc_dtype dtype, int64_t tokens, int32_t heads, int32_t d, void *stream);
+
+/*
+ * kv_append -- writes k, v [tokens, hkv, d] to their sequences' slots.  strides:
+ * {k token, k head, v token, v head, q token, q head}, in elements, multiples
+ * of 8.  rope (may be NULL: no rotation) turns k by positions [tokens], or by
+ * the slots where positions is NULL; with q not NULL the same launch writes
+ * q_out [tokens, hq, d] (contiguous) = q turned alike.
+ * Scale of a (page, head, side) that gets tokens: the least 2^e with amax <=
+ * 448 * 2^e, e in [-15, 7] (fp16) or [-100, 119] (bf16), so that code * scale is
+ * exactly a value of the type; amax is over the finite new values (k's after
+ * its rotation, in fp32).  A page that keeps earlier tokens takes the larger of
+ * that and its present scale, and where it grows its earlier codes are rounded
+ * again.  code = e4m3 of the value / scale, saturated to +-448, nearest even.
+ * A NaN of k is stored as NaN; a token with a NaN in v has those stored as 0 and
+ * a NaN in its k, so that the queries that see the token, and no others, turn
+ * NaN.  Slots past the new length, and pages that get no token, keep their bytes.
+ */
+fc_status kv_append(const void *k, const void *v, const void *q, void *q_out, const int64_t *strides,
+                    uint8_t *codes, float *scales, const int32_t *table, const int32_t *cu_q,
+                    const int32_t *kv_lens, const int32_t *positions, const fc_rope *rope,
+                    const fc_kv_shape *shape, void *stream);
+
+/* Kernel forms of chain_attn: ROWS for few rows (new tokens x the heads that
+ * share a kv head; the keys are split over waves and blocks), TILE for many
+ * (codes staged through LDS for 128 rows).  Both compute the same values up to
+ * the order of fp32 sums. */
+typedef enum { FC_ATTN_AUTO = 0, FC_ATTN_ROWS = 1, FC_ATTN_TILE = 2 } fc_attn_variant;
+
+typedef struct {
+    float scale;        /* > 0: scores are scale * q . k */
+    float softcap;      /* > 0: softcap * tanh(score / softcap); 0: off */
+    int32_t causal;     /* != 0: the query at slot s sees slots <= s */
+    int32_t window;     /* > 0: it sees the last `window` of them (causal only); 0: all */
+    int32_t variant;    /* fc_attn_variant */
+    int32_t splits;     /* blocks a sequence's keys are split over; 0: chosen */
+} fc_attn_params;
+
+typedef struct {
+    int32_t variant, splits, chunk;   /* chunk: keys a split */
+    int64_t workspace;                /* bytes chain_attn needs (0 when splits == 1) */
+} fc_attn_plan;
+
+/* The form, split and workspace of a call (host only). */
+fc_status chain_attn_plan(const fc_kv_shape *shape, const fc_attn_params *params, fc_attn_plan *plan);
+
+/*
+ * chain_attn -- out [tokens, hq, d] = softmax(scores) V over the cache, scores
+ * as in fc_attn_params, minus slopes[head] * |query slot - key slot| where
+ * slopes [hq] is not NULL (after the cap).  A row that sees no key (an empty
+ * sequence) is 0 and its lse -inf; lse [tokens, hq] (may be NULL) is the
+ * natural logarithm of the sum of exponentials.  strides {q token, q head},
+ * multiples of 8.  The scores never reach memory; weights are rounded once to
+ * the activations' type, everything else of the softmax is fp32.  workspace:
+ * device memory of chain_attn_plan's size, 16-byte aligned, not shared by calls
+ * that may run at once.  Rows that belong to no sequence hold nothing defined.
+ * d: see fc_kv_shape (others FC_E_UNSUPPORTED).
+ */
+fc_status chain_attn(const void *q, const int64_t *strides, const uint8_t *codes, const float *scales,
+                     const int32_t *table, const int32_t *cu_q, const int32_t *kv_lens, const float *slopes,
+                     const fc_attn_params *params, void *out, float *lse, const fc_kv_shape *shape,
+                     void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * kv_check -- looks HOST copies of a batch's metadata over: cu_q starts at 0,
+ * does not fall and ends within tokens; every length is within its sequence's
+ * new tokens and its table row; every page id it needs is inside the pool; with
+ * writes != 0, no page that gets new tokens is also another sequence's.
+ * FC_E_SHAPE with the first fault's place in fc_last_error.  Launches nothing.
+ */
+fc_status kv_check(const int32_t *table, const int32_t *cu_q, const int32_t *kv_lens, const fc_kv_shape *shape,
+                   int32_t writes);
+
 /* ---- input preparation (BOLT notes, "Templated code generation": tensors
  *      whose channel count is not a multiple of 8 are zero-padded) ----
  * dst[o][j][i] = j < c_in ? src[o][j][i] : 0 for a tensor viewed as
