@@ -249,6 +249,7 @@ fc_status chain_attn(const void* q, const int64_t* strides, const uint8_t* codes
     a.window = params->window;
     a.nsplit = p.splits;
     a.chunk = p.chunk / 16;
+    a.pg_shift = __builtin_ctz((unsigned)shape->page) - 4;
     a.scale = params->scale;
     a.cap = params->softcap;
     a.by_g = fc::FastDiv::make(a.G);

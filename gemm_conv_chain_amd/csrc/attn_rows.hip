@@ -86,18 +86,17 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
                 for (int d = 0; d < ND; ++d) o[c][d] = floatx4{0, 0, 0, 0};
             }
 
-            const int per_page = s.page >> 4;
             for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
                 const int c1 = c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
                 for (int k0 = c0 + 4 * wave; k0 < c1; k0 += 4 * AR_WAVES) {
                     // the blocks of this lane: K rows of block n >> 2, scores and V of block g
                     const int gk = k0 + (n >> 2) < c1 ? k0 + (n >> 2) : c1 - 1;
                     const int gv = k0 + g < c1 ? k0 + g : c1 - 1;
-                    const int pk = gk / per_page, pv = gv / per_page;
+                    const int pk = gk >> a.pg_shift, pv = gv >> a.pg_shift;
                     const int idk = page_id(a.table, s, b, pk), idv = page_id(a.table, s, b, pv);
-                    const uint8_t* kb = a.codes + side_base(idk < 0 ? 0 : idk, h, 0, s) + (gk - pk * per_page) * (16 * D) +
+                    const uint8_t* kb = a.codes + side_base(idk < 0 ? 0 : idk, h, 0, s) + (gk - (pk << a.pg_shift)) * (16 * D) +
                                         g * 256 + (n & 3) * 16;
-                    const uint8_t* vb = a.codes + side_base(idv < 0 ? 0 : idv, h, 1, s) + (gv - pv * per_page) * (16 * D) +
+                    const uint8_t* vb = a.codes + side_base(idv < 0 ? 0 : idv, h, 1, s) + (gv - (pv << a.pg_shift)) * (16 * D) +
                                         n * 16;
                     u32x4 kr[4][NJ], vr[ND];
 #pragma unroll
@@ -267,29 +266,53 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
     }
 }
 
-// One wave a row: the splits' results weighted by 2^(m - max m).  A split that
-// saw no key has l = 0 and has written no o.
-template <class T>
+// Joins the splits of a row by weights 2^(m - max m): WPR waves a row, a lane D /
+// 64 of its elements, a wave every WPR-th split.  A split that saw no key has l =
+// 0 and has written no o: what its place holds is loaded but not used.
+template <class T, int WPR>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 {
-    const int lane = threadIdx.x & 63, D = a.s.d;
-    const long row = (long)blockIdx.x * 4 + (threadIdx.x >> 6);
-    if (row >= rows) return;
-    const float* ml = a.part_ml + row * a.nsplit * 2;
+    __shared__ float part[WPR > 1 ? WPR - 1 : 1][5][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % WPR, D = a.s.d;
+    const long row = (long)blockIdx.x * (4 / WPR) + wave / WPR;
+    const bool live = row < rows;
+    const floatx2* ml = reinterpret_cast<const floatx2*>(a.part_ml) + (live ? row : 0) * a.nsplit;
     float m = kNegInf;
-    for (int k = 0; k < a.nsplit; ++k) m = fmaxf(m, ml[2 * k]);
+    for (int k = lane; k < a.nsplit; k += 64) m = fmaxf(m, ml[k][0]);
+#pragma unroll
+    for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
     const float ms = m == kNegInf ? 0.0f : m;
     float l = 0.0f, o[4] = {0, 0, 0, 0};
-    for (int k = 0; k < a.nsplit; ++k) {
-        const float lk = ml[2 * k + 1];
-        if (lk == 0.0f) continue;
-        const float f = __builtin_amdgcn_exp2f(ml[2 * k] - ms);
-        l += lk * f;
-        const float* p = a.part_o + (row * a.nsplit + k) * D;
+    const float* p = a.part_o + (live ? row : 0) * a.nsplit * D + lane;
+#pragma unroll 4
+    for (int k = w; k < a.nsplit; k += WPR) {
+        const floatx2 v = ml[k];
+        const float f = __builtin_amdgcn_exp2f(v[0] - ms);
+        const bool some = v[1] != 0.0f;
+        l += some ? v[1] * f : 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i * 64 < D) o[i] += p[i * 64 + lane] * f;
+            if (i * 64 < D) {
+                const float y = p[(long)k * D + i * 64] * f;
+                o[i] += some ? y : 0.0f;
+            }
     }
+    if (WPR > 1) {   // in the waves' order, whatever their timing
+        if (w > 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) part[w - 1][i][lane] = o[i];
+            part[w - 1][4][lane] = l;
+        }
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int j = 0; j < WPR - 1; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] += part[j][i][lane];
+            l += part[j][4][lane];
+        }
+    }
+    if (!live) return;
     const float inv = l != 0.0f ? 1.0f / l : 0.0f;
     T* out = (T*)a.out + row * D;
 #pragma unroll
@@ -337,13 +360,19 @@ hipError_t run_attn_rows(int dtype, const AttnArgs& a, hipStream_t st)
     return dtype == DT_F16 ? rows_by_d<half_t>(a, st) : rows_by_d<bf16_t>(a, st);
 }
 
-hipError_t run_attn_join(int dtype, const AttnArgs& a, hipStream_t st)
+// Many splits come with few rows: the waves of a block share a row then.
+template <class T>
+static hipError_t launch_join(const AttnArgs& a, hipStream_t st)
 {
     const long rows = a.s.tokens * a.s.hq;
-    const dim3 grid((unsigned)((rows + 3) / 4));
-    if (dtype == DT_F16) k_attn_join<half_t><<<grid, dim3(256), 0, st>>>(a, rows);
-    else k_attn_join<bf16_t><<<grid, dim3(256), 0, st>>>(a, rows);
+    if (a.nsplit > 8) k_attn_join<T, 4><<<dim3((unsigned)rows), dim3(256), 0, st>>>(a, rows);
+    else k_attn_join<T, 1><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(a, rows);
     return hipGetLastError();
+}
+
+hipError_t run_attn_join(int dtype, const AttnArgs& a, hipStream_t st)
+{
+    return dtype == DT_F16 ? launch_join<half_t>(a, st) : launch_join<bf16_t>(a, st);
 }
 
 }  // namespace fc

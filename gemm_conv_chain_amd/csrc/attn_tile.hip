@@ -7,44 +7,83 @@
 // its partner l ^ 32 (running maximum and sum in 32 bits), and p, rounded once
 // to the activations' type, straight from the accumulators into operand B of
 // O^T += V^T p^T.  Accumulator row 8b + 4h + i of lane half h is key 16h + 4b
-// + i of a 32-key subtile, so that a half's 16 keys are one cache block and
-// its V operand is 16 consecutive bytes.
+// + i of a 32-key subtile, so that a half's 16 keys are one cache block.
 //
-// Codes go to LDS as they are (8 bits), 64 keys a stage by LDS-DMA, the next
-// stage in flight during a stage's products; a wave widens them in registers
-// as operands.  The blocks of 16 keys sit 16 * D + 128 bytes apart, so that the
-// 16 lanes of a fragment read that straddle two blocks meet all 64 banks.
-#include "fc_dma.h"
+// Keys pass through LDS 64 a stage, widened once for the whole block: a wave
+// loads its share of the codes two stages ahead, widens it (times the page's
+// scale, which is exact) and writes it in operand order while the block
+// computes the stage before.  Every wave widening its own operands from 8-bit
+// codes in LDS, as this kernel first did, cost 128 of ~430 vector instructions
+// a wave and stage, and vector issue is what bounds it.
 #include "fc_launch.h"
 #include "kv_common.h"
 
 namespace fc {
 
 typedef FC_LDS uint8_t lds_u8;
-typedef __attribute__((address_space(4))) const int const_int;
-typedef __attribute__((address_space(4))) const float const_float;
 
-template <class T, int D, int NW, bool CAP>
-__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArgs a, int row_tiles)
+// Scores of the first kind: scale * q . k alone; with a bias by distance; capped
+// (with or without a bias), or not causal with one.
+enum { SC_PLAIN = 0, SC_BIAS = 1, SC_ANY = 2 };
+
+// What a page outside the pool is read as: NaN keys, so that the rows that see
+// them turn NaN and no others, and zero values.
+struct NoPage {
+    unsigned codes[2][1024];
+    float scale[2];
+};
+__host__ __device__ constexpr NoPage make_no_page()
+{
+    NoPage p{};
+    for (int i = 0; i < 1024; ++i) p.codes[0][i] = 0x7f7f7f7fu;
+    p.scale[0] = p.scale[1] = 1.0f;
+    return p;
+}
+static __device__ __align__(16) NoPage fc_no_page = make_no_page();
+
+// Waves a block and blocks of 16 keys a stage.  Heads of 192 and 256 leave a SIMD
+// room for two waves only if a block of eight shares the widening (d = 192: 220
+// us, against 401 with four waves of 512 registers, for two prompts of 4096 and
+// 16 heads), and of 256 only with stages of 32 keys (355 us against 518 with 64,
+// whose scores spill).
+__host__ __device__ constexpr int tile_waves(int d) { return d <= 128 ? 4 : 8; }
+__host__ __device__ constexpr int tile_blocks(int d) { return d <= 192 ? 4 : 2; }
+
+template <class T, int D, int NW, int MODE>
+__global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_tiles)
 {
     typedef typename Tr<T>::v8 v8;
-    constexpr int GB = 16 * D + 128;       // bytes from block to block of 16 keys in LDS
-    constexpr int STAGE = 8 * GB;          // 4 blocks of K, 4 of V
-    constexpr int NJ = D / 32, ND = D / 32, NP = D / 64;
-    static_assert(NW == 4 || NW == 8, "a wave fetches a whole block of 16 keys or one side of it");
+    constexpr int BR = 32 * NW;              // rows a block
+    constexpr int KB = tile_blocks(D), U = KB / 2;   // blocks of 16 keys a stage, subtiles of 32
+    constexpr int SIDE = 16 * KB * D * 2;    // bytes of a stage's keys (or values), 16 bits each
+    constexpr int STAGE = 2 * SIDE;
+    constexpr int NK = D / 16, ND = D / 32, NP = D / 64;
+    constexpr int PW = 2 * KB * NP / NW;     // pieces of 1 KiB of codes a wave and stage
+    static_assert(2 * KB * NP % NW == 0 && 2 * NP % PW == 0, "a wave's pieces are of one block");
+    constexpr int AH = 2;     // operands read ahead
     const KvShape& s = a.s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
-    const int h = blockIdx.y, split = blockIdx.x % a.nsplit;
-    const int rt0 = row_tiles - 1 - (int)(blockIdx.x / a.nsplit);   // long rows (causal) first
+    const int h = blockIdx.x, split = blockIdx.y % a.nsplit;
+    const int rt0 = row_tiles - 1 - (int)(blockIdx.y / a.nsplit);   // long rows (causal) first
 
-    __shared__ __align__(16) uint8_t buf[2 * STAGE];
-    __shared__ float sc_lds[2][4][2];
+    extern __shared__ __align__(16) uint8_t buf[];
     lds_u8* const lb = (lds_u8*)buf;
     if constexpr (kPoison) {
         lds_poison(lb, 2 * STAGE, threadIdx.x, 64 * NW);
         __syncthreads();
     }
+    const NoPage* no_page = &fc_no_page;
+    asm("" : "+s"(no_page));   // the address is taken once, not by a load in every stage
+    // This wave's share of a stage: PW pieces of one of its blocks.  A
+    // K row of 16 dims of a token goes to row m of the operand; the swap of
+    // fours in every other row lets a write meet all the banks.
+    const int blk = wave * PW / (2 * NP), piece0 = wave * PW % (2 * NP);   // piece: side * NP + p
+    const int tok = lane & 15;
+    const int k_to = (blk >> 1) * (SIDE / U) + (lane >> 4) * 1024 +
+                     ((8 * (tok >> 2) + 4 * (blk & 1) + (tok & 3)) ^ (4 * ((lane >> 4) & 1))) * 16;
+    const int v_to = SIDE + ((blk >> 1) * 4 + (blk & 1)) * (16 * D) + lane * 16;
+    const int k_at = hf * 1024 + (n ^ (4 * hf)) * 16, v_at = SIDE + hf * (16 * D) + n * 16;
 
     for (int b = blockIdx.z; b < s.batch; b += gridDim.z) {
         long tok0;
@@ -53,8 +92,11 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArg
         const int rows = nq * a.G;
         bool over;
         const int kv_len = seq_keys(a.kv_lens, s, b, &over), pos0 = kv_len - nq;
-        for (int r0 = rt0 * 32 * NW; r0 < rows; r0 += row_tiles * 32 * NW) {
-            const int r1 = r0 + 32 * NW < rows ? r0 + 32 * NW : rows;
+        const int* const row_of = a.table + (size_t)b * s.table_stride;
+        const uint8_t* const head = a.codes + side_base(0, h, 0, s);
+        const size_t page_bytes = (size_t)s.hkv * 2 * s.page * D;
+        for (int r0 = rt0 * BR; r0 < rows; r0 += row_tiles * BR) {
+            const int r1 = r0 + BR < rows ? r0 + BR : rows;
             int g_lo, g_hi;
             key_range(a, kv_len, pos0, a.by_g.div(r0), a.by_g.div(r1 - 1), &g_lo, &g_hi);
             // this wave's rows
@@ -68,128 +110,194 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArg
             // this lane's row
             const int r = w0 + n, rr = r < rows ? r : rows - 1;
             const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G), pos = pos0 + t;
-            const int hi = a.causal ? (pos + 1 < kv_len ? pos + 1 : kv_len) : kv_len;
-            const int lo = a.window > 0 ? pos - a.window + 1 : 0;
-            const float slope = a.slopes ? a.slopes[hq] * kLog2e : 0.0f, posf = (float)pos;
-            v8 qf[2 * NJ];
+            const float slope = MODE != SC_PLAIN && a.slopes ? a.slopes[hq] * (MODE == SC_BIAS ? 1.0f / a.scale : kLog2e) : 0.0f;
+            v8 qf[NK];
             {
                 const T* q = (const T*)a.q + (tok0 + t) * a.q_ts + (long)hq * a.q_hs;
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) qf[2 * j + e] = *reinterpret_cast<const v8*>(q + 16 * (2 * j + hf) + 8 * e);
+                for (int j = 0; j < NK; ++j) qf[j] = *reinterpret_cast<const v8*>(q + 16 * (2 * (j >> 1) + hf) + 8 * (j & 1));
             }
+            // x * unit: the exponent of 2; of the general kind x is that already
+            const float unit = MODE == SC_ANY ? 1.0f : a.scale * kLog2e, lag = 8.0f / unit;
+            const float cap0 = 2.0f * kLog2e * a.scale / (a.cap > 0.0f ? a.cap : 1.0f);
             floatx16 o[ND];
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] = zero16();
-            float m = kNegInf, l = 0.0f;
+            float m = kNegInf, mb = 0.0f, l = 0.0f;   // the maximum that weights refer to; with 0 for -inf
 
-            const int per_page = s.page >> 4;
             for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
                 const int c1 = c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
-                // requests of this wave for the stage that begins at block k0
-                auto fetch = [&](int k0, int stage) {
-                    const int gi = NW == 4 ? wave : wave >> 1;
-                    const int gk = k0 + gi < c1 ? k0 + gi : c1 - 1;
-                    const int pg = gk / per_page;
-                    int id = -1;
-                    if ((unsigned)pg < (unsigned)s.table_stride) id = ((const_int*)a.table)[(size_t)b * s.table_stride + pg];
-                    const bool ok = (unsigned)id < (unsigned)s.pages;
+                // Loads of this wave's share of the stage at block k0, the page's id already here.
+                auto block_of = [&](int k0) { return k0 + blk < c1 ? k0 + blk : c1 - 1; };
+                auto load_id = [&](int k0) {
+                    const int pg = block_of(k0) >> a.pg_shift;
+                    return row_of[pg < s.table_stride ? pg : 0];
+                };
+                u32x4 raw[PW];
+                float sc[PW];
+                auto load = [&](int k0, int idv) {
+                    const int gk = block_of(k0), pg = gk >> a.pg_shift;
+                    int id = __builtin_amdgcn_readfirstlane(idv);
+                    const bool ok = (unsigned)id < (unsigned)s.pages && pg < s.table_stride;
                     id = ok ? id : 0;
-                    const int inpage = (gk - pg * per_page) * (16 * D);
+                    const uint8_t* src = head + id * page_bytes + (gk - (pg << a.pg_shift)) * (16 * D);
+                    const float* scale = a.scales + ((size_t)id * s.hkv + h) * 2;
+                    // (the choice is on the addresses: one on the values would wait for the loads)
+                    scale = ok ? scale : no_page->scale;
 #pragma unroll
-                    for (int sd = 0; sd < 2; ++sd) {
-                        if (NW == 8 && sd != (wave & 1)) continue;
-                        const i32x4 rs = buf_rsrc(a.codes + side_base(id, h, sd, s) + inpage, ok ? 16 * D : 0);   // none: zeros
-                        lds_u8* dst = lb + stage * STAGE + (sd * 4 + gi) * GB;
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) {
-                            if (kPoison) dma16(buf_rsrc(&fc_poison_line, 1024), lane * 16, (const lds_half*)(dst + p * 1024));
-                            dma16(rs, p * 1024 + lane * 16, (const lds_half*)(dst + p * 1024));
-                        }
-                        const float v = ((const_float*)a.scales)[((size_t)id * s.hkv + h) * 2 + sd];
-                        // a page outside the pool: every row that sees its keys turns NaN
-                        if (lane == 0) sc_lds[stage][gi][sd] = ok ? v : (sd ? 1.0f : __builtin_nanf(""));
+                    for (int i = 0; i < PW; ++i) {
+                        const int side = (piece0 + i) / NP, p = (piece0 + i) % NP;
+                        sc[i] = scale[side];
+                        const uint8_t* from = ok ? src + side * (s.page * D) : (const uint8_t*)no_page->codes[side];
+                        raw[i] = *reinterpret_cast<const u32x4*>(from + p * 1024 + lane * 16);
                     }
                 };
+                // weight 0 times a NaN code past the end would be NaN: those codes are cleared
+                auto clear_tail = [&](int k0) {
+                    const int keep = kv_len - (k0 + blk) * 16;   // tokens of the block that there are
+                    if (keep >= 16) return;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int k = keep - 4 * j;
+                        const unsigned mk = k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+#pragma unroll
+                        for (int i = 0; i < PW; ++i) raw[i][j] &= piece0 + i < NP ? ~0u : mk;
+                    }
+                };
+                // half i & 1 of piece i >> 1: eight codes a lane
+                auto widen = [&](int stage, int i) {
+                    const int pc = piece0 + (i >> 1), p = pc % NP, e = i & 1;
+                    FC_LDS u32x4* d = (FC_LDS u32x4*)(lb + stage * STAGE + (pc >= NP ? v_to + p * 1024 + e * (32 * D)
+                                                                                     : k_to + p * 4096 + e * 512));
+                    if (kPoison) *d = u32x4{kPoisonWord, kPoisonWord, kPoisonWord, kPoisonWord};
+                    *d = __builtin_bit_cast(u32x4, frag8<T>(raw[i >> 1][2 * e], raw[i >> 1][2 * e + 1], sc[i >> 1]));
+                };
+                constexpr int PARTS = 2 * PW;
+                int id = load_id(c0);
+                load(c0, id);
+                id = load_id(c0 + KB);
                 __syncthreads();   // the buffers are free
-                fetch(c0, 0);
-                for (int k0 = c0, stage = 0; k0 < c1; k0 += 4, stage ^= 1) {
-                    vm_wait<0>();
-                    __syncthreads();   // this stage has arrived, and every wave is done with the other one
-                    if (k0 + 4 < c1) fetch(k0 + 4, stage ^ 1);
-                    if (!live || k0 >= wg_hi || k0 + 4 <= wg_lo) continue;
-                    const lds_u8* kb = lb + stage * STAGE + ((n >> 2) & 1) * GB + (4 * (n >> 3) + (n & 3)) * 16 + hf * 256;
-                    const lds_u8* vb = lb + stage * STAGE + (4 + hf) * GB + n * 16;
-                    float x[32];
+                clear_tail(c0);
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        floatx16 acc = zero16();
+                for (int i = 0; i < PARTS; ++i) widen(0, i);
+                load(c0 + KB, id);
+                id = load_id(c0 + 2 * KB);
+                for (int k0 = c0, stage = 0; k0 < c1; k0 += KB, stage ^= 1) {
+                    __syncthreads();   // this stage is here, and every wave is done with the other one
+                    // the next stage's share is widened between this one's products (after the
+                    // last stage to no purpose)
+                    clear_tail(k0 + KB);
+                    if (!live || k0 >= wg_hi || k0 + KB <= wg_lo) {
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            const u32x4 w = *reinterpret_cast<const FC_LDS u32x4*>(kb + 2 * u * GB + j * 512);
-                            acc = Tr<T>::mfma32(frag8<T>(w[0], w[1], 1.0f), qf[2 * j], acc);
-                            acc = Tr<T>::mfma32(frag8<T>(w[2], w[3], 1.0f), qf[2 * j + 1], acc);
-                        }
-                        const float ks = sc_lds[stage][2 * u + hf][0];
-                        const float c0s = CAP ? 2.0f * kLog2e * ks * a.scale / a.cap : ks * a.scale * kLog2e;
-                        const float c1s = a.cap * kLog2e;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[16 * u + i] = score<CAP>(acc[i], c0s, c1s);
+                        for (int i = 0; i < PARTS; ++i) widen(stage ^ 1, i);
+                        load(k0 + 2 * KB, id);
+                        id = load_id(k0 + 3 * KB);
+                        continue;
                     }
+                    const lds_u8* const kb = lb + stage * STAGE + k_at;
+                    const lds_u8* const vb = lb + stage * STAGE + v_at;
                     const int key0 = k0 * 16 + 16 * hf;
-                    if (a.slopes) {
-                        const float gap = posf - (float)key0;
+                    // The accumulators begin at minus the reference maximum (and the bias), so that
+                    // the products come out as the exponent's argument, up to its factor.
+                    floatx16 x[U];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] -= slope * fabsf(gap - (float)((i >> 4) * 32 + (i & 15)));
+                    for (int u = 0; u < U; ++u) {
+                        const float base = MODE == SC_BIAS ? slope * (float)(key0 + 32 * u - pos) - mb
+                                           : MODE == SC_PLAIN ? -mb : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[u][i] = MODE == SC_BIAS ? __builtin_fmaf(slope, (float)i, base) : base;
                     }
-                    if (k0 * 16 < all_lo || (k0 + 4) * 16 > all_hi || k0 + 4 > c1) {
-                        const int top = hi < c1 * 16 ? hi : c1 * 16;
+                    // Operands are read AH products ahead, the first of V before the softmax; the
+                    // barriers keep the compiler from sinking each read to its use.
+                    constexpr int NF = U * NK, NV = KB * ND;
+                    auto k_read = [&](int i) {   // subtile i % U, dims of step i / U
+                        const int j = i / U;
+                        return *reinterpret_cast<const FC_LDS v8*>(kb + i % U * (SIDE / U) + (j >> 1) * 2048 + (j & 1) * 512);
+                    };
+                    auto v_read = [&](int i) {   // keys of step i / ND, dims of tile i % ND
+                        return *reinterpret_cast<const FC_LDS v8*>(vb + (i / ND) * (32 * D) + (i % ND) * 512);
+                    };
+                    v8 kf[NF], vf[NV];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int key = key0 + (i >> 4) * 32 + (i & 15);
-                            x[i] = key < top && key >= lo ? x[i] : kNegInf;
+                    for (int i = 0; i < AH; ++i) kf[i] = k_read(i);
+#pragma unroll
+                    for (int g = 0; g < NF; g += AH) {
+#pragma unroll
+                        for (int i = g; i < g + AH; ++i) {
+                            if (i + AH < NF) kf[i + AH] = k_read(i + AH);
+                            else vf[i + AH - NF] = v_read(i + AH - NF);
                         }
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int i = g; i < g + AH; ++i) {
+                            x[i % U] = Tr<T>::mfma32(kf[i], qf[i / U], x[i % U]);
+                            if (i * PARTS / NF != (i + 1) * PARTS / NF) widen(stage ^ 1, i * PARTS / NF);
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    float mx = x[0];
+                    load(k0 + 2 * KB, id);
+                    id = load_id(k0 + 3 * KB);
+                    if (MODE == SC_ANY) {
 #pragma unroll
-                    for (int i = 1; i < 32; ++i) mx = fmaxf(mx, x[i]);
-                    mx = max_x32(mx);
-                    const float mn = fmaxf(m, mx), ms = mn == kNegInf ? 0.0f : mn;
-                    const float alpha = __builtin_amdgcn_exp2f(m - ms);
-                    m = mn;
-                    float sum = 0.0f;
-                    u32x4 w[4];
+                        for (int u = 0; u < U; ++u) {
+                            const float gap = (float)(pos - key0 - 32 * u);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        const float p0 = __builtin_amdgcn_exp2f(x[i] - ms), p1 = __builtin_amdgcn_exp2f(x[i + 1] - ms);
-                        sum += p0 + p1;
-                        w[i >> 3][(i >> 1) & 3] = Tr<T>::pk(p0, p1);
-                    }
-                    l = l * alpha + sum;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) o[d] *= alpha;
-                    const bool tail = (k0 + 4) * 16 > kv_len;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float vs = sc_lds[stage][2 * u + hf][1];
-                        u32x4 mk = {~0u, ~0u, ~0u, ~0u};
-                        if (tail) {   // tokens past the end: weight 0, but their codes may be NaN
-                            const int keep = kv_len - key0 - 32 * u;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int k = keep - 4 * j;
-                                mk[j] = k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+                            for (int i = 0; i < 16; ++i) {
+                                const float y = a.cap > 0.0f ? score<true>(x[u][i], cap0, a.cap * kLog2e) : x[u][i] * (a.scale * kLog2e);
+                                x[u][i] = (y - slope * fabsf(gap - (float)i)) - mb;
                             }
                         }
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) {
-                            u32x4 c = *reinterpret_cast<const FC_LDS u32x4*>(vb + 2 * u * GB + d * 512);
-                            if (tail) c &= mk;
-                            o[d] = Tr<T>::mfma32(frag8<T>(c[0], c[1], vs), __builtin_bit_cast(v8, w[2 * u]), o[d]);
-                            o[d] = Tr<T>::mfma32(frag8<T>(c[2], c[3], vs), __builtin_bit_cast(v8, w[2 * u + 1]), o[d]);
-                        }
                     }
+                    if (k0 * 16 < all_lo || (k0 + KB) * 16 > all_hi || k0 + KB > c1) {
+                        int top = a.causal && pos + 1 < kv_len ? pos + 1 : kv_len;
+                        top = (top < c1 * 16 ? top : c1 * 16) - key0;
+                        const int low = (a.window > 0 ? pos - a.window + 1 : 0) - key0;
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) x[u][i] = 32 * u + i < top && 32 * u + i >= low ? x[u][i] : kNegInf;
+                    }
+                    float mx = x[0][0];
+#pragma unroll
+                    for (int i = 1; i < 16 * U; ++i) mx = fmaxf(mx, x[i >> 4][i & 15]);
+                    mx = max_x32(mx) + mb;
+                    // Weights refer to a maximum that may lag by a factor of 2^8, so that most stages do
+                    // not touch the accumulators: a weight is at most 256, as exact as one of at most 1.
+                    if (__any(mx > m + lag)) {
+                        const float mn = fmaxf(m, mx), to = mn == kNegInf ? 0.0f : mn;
+                        const float by = to - mb;
+                        const float alpha = __builtin_amdgcn_exp2f((m - to) * unit);
+                        m = mn;
+                        mb = to;
+                        l *= alpha;
+#pragma unroll
+                        for (int d = 0; d < ND; ++d) o[d] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < 16 * U; ++i) x[i >> 4][i & 15] -= by;
+                    }
+                    // weights and second product by turns: the products with 8 keys' weights, and
+                    // between them the weights of the next 8
+                    float sum = 0.0f;
+                    u32x4 w[KB];
+                    auto weigh = [&](int i) {
+                        const float p0 = __builtin_amdgcn_exp2f(x[i >> 3][2 * (i & 7)] * unit);
+                        const float p1 = __builtin_amdgcn_exp2f(x[i >> 3][2 * (i & 7) + 1] * unit);
+                        sum += p0 + p1;
+                        w[i >> 2][i & 3] = Tr<T>::pk(p0, p1);
+                    };
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) weigh(i);
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) {
+                        if (i + AH < NV) vf[i + AH] = v_read(i + AH);
+                        o[i % ND] = Tr<T>::mfma32(vf[i], __builtin_bit_cast(v8, w[i / ND]), o[i % ND]);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (i / ND < KB - 1 && k * ND / 4 == i % ND) weigh(4 * (i / ND + 1) + k);
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+                    l += sum;
                 }
             }
             l = over ? __builtin_nanf("") : sum_x32(l);
@@ -202,12 +310,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArg
                     for (int d = 0; d < ND; ++d)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            u32x2 w;
-                            w[0] = Tr<T>::pk(o[d][4 * k] * inv, o[d][4 * k + 1] * inv);
-                            w[1] = Tr<T>::pk(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv);
-                            *reinterpret_cast<u32x2*>(out + 32 * d + 8 * k) = w;
+                            u32x2 v;
+                            v[0] = Tr<T>::pk(o[d][4 * k] * inv, o[d][4 * k + 1] * inv);
+                            v[1] = Tr<T>::pk(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv);
+                            *reinterpret_cast<u32x2*>(out + 32 * d + 8 * k) = v;
                         }
-                    if (a.lse && hf == 0) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * (1.0f / kLog2e);
+                    if (a.lse && hf == 0) a.lse[row] = (m * unit + __builtin_amdgcn_logf(l)) * (1.0f / kLog2e);
                 } else {
                     const long at = row * a.nsplit + split;
                     if (l != 0.0f) {
@@ -220,7 +328,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArg
                                     floatx4{o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]};
                     }
                     if (hf == 0) {
-                        a.part_ml[at * 2] = m;
+                        a.part_ml[at * 2] = m * unit;
                         a.part_ml[at * 2 + 1] = l;
                     }
                 }
@@ -229,27 +337,38 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_tile(AttnArg
     }
 }
 
-template <class T, int D, bool CAP>
+template <class T, int D, int MODE>
 static hipError_t launch_tile(const AttnArgs& a, hipStream_t st)
 {
-    constexpr int NW = 4;
+    constexpr int NW = tile_waves(D);
+    static std::atomic<unsigned long long> done{0};
+    hipError_t e = allow_full_lds((const void*)k_attn_tile<T, D, NW, MODE>, &done);
+    if (e != hipSuccess) return e;
     const long rows = (long)(a.s.max_q > 0 ? a.s.max_q : 1) * a.G;
     long rt = (rows + 32 * NW - 1) / (32 * NW);
-    if (rt * a.nsplit > 0x7fffffffL) rt = 0x7fffffffL / a.nsplit;
-    const dim3 grid((unsigned)(rt * a.nsplit), a.s.hkv, a.s.batch < 65535 ? a.s.batch : 65535);
-    k_attn_tile<T, D, NW, CAP><<<grid, dim3(64 * NW), 0, st>>>(a, (int)rt);
+    if (rt * a.nsplit > 65535) rt = 65535 / a.nsplit;
+    // heads fastest: workgroups go round-robin over the 8 XCDs, so that the row
+    // tiles of a head, which read the same codes, meet in one L2 (hkv % 8 == 0)
+    const dim3 grid(a.s.hkv, (unsigned)(rt * a.nsplit), a.s.batch < 65535 ? a.s.batch : 65535);
+    k_attn_tile<T, D, NW, MODE><<<grid, dim3(64 * NW), 2 * 2 * 16 * tile_blocks(D) * D * 2, st>>>(a, (int)rt);
     return hipGetLastError();
+}
+
+template <class T, int D>
+static hipError_t tile_mode(const AttnArgs& a, hipStream_t st)
+{
+    if (a.cap > 0.0f || (a.slopes && !a.causal)) return launch_tile<T, D, SC_ANY>(a, st);
+    return a.slopes ? launch_tile<T, D, SC_BIAS>(a, st) : launch_tile<T, D, SC_PLAIN>(a, st);
 }
 
 template <class T>
 static hipError_t tile_by_d(const AttnArgs& a, hipStream_t st)
 {
-    const bool cap = a.cap > 0.0f;
     switch (a.s.d) {
-    case 64: return cap ? launch_tile<T, 64, true>(a, st) : launch_tile<T, 64, false>(a, st);
-    case 128: return cap ? launch_tile<T, 128, true>(a, st) : launch_tile<T, 128, false>(a, st);
-    case 192: return cap ? launch_tile<T, 192, true>(a, st) : launch_tile<T, 192, false>(a, st);
-    default: return cap ? launch_tile<T, 256, true>(a, st) : launch_tile<T, 256, false>(a, st);
+    case 64: return tile_mode<T, 64>(a, st);
+    case 128: return tile_mode<T, 128>(a, st);
+    case 192: return tile_mode<T, 192>(a, st);
+    default: return tile_mode<T, 256>(a, st);
     }
 }
 

@@ -262,6 +262,7 @@ struct AttnArgs {
     float *part_o, *part_ml;   // workspace of nsplit > 1: [tokens, hq, nsplit, d] and [.., 2]
     KvShape s;
     int G, causal, window, nsplit, chunk;   // chunk: blocks of 16 keys a split
+    int pg_shift;                            // a page holds 2^pg_shift blocks of 16
     float scale, cap;
     FastDiv by_g;
 };
