@@ -125,34 +125,54 @@ int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p)
     return (keys + 15) / 16 + 1;
 }
 
-// Few rows take the form whose waves split the keys; 33 and more fill a tile of
-// 128 well enough that reading the codes once for all of them wins.  Keys are
-// split over blocks until the launch has about `want` of them.
+// Form and split of a call.  Few rows take the form whose waves split the keys,
+// more the one that stages them for a tile of rows; where they meet depends on
+// whether sequences x kv heads alone fill the machine (us, rows form / tile form):
+//   32 x 4, 8000 keys    d = 64    16 rows 36 / 37     32 rows 46 / 38
+//                        d = 128   32 rows 57 / 65     64 rows 91 / 83
+//                        d = 256   64 rows 187 / 304   128 rows 338 / 340
+//   8 x 4, 4000 keys     d = 64    64 rows 19 / 21     128 rows 26 / 24
+//                        d = 128   64 rows 24 / 29     96 rows 38 / 31
+//                        d = 256   64 rows 49 / 60     96 rows 77 / 63
+// Keys are split over blocks where rows and heads alone leave CUs without one
+// (us, by splits):
+//   rows, 2 sequences x 4 heads, 131071 keys    8: 126   16: 71   32: 52   64: 59
+//   rows, 64 x 8, to 8192 keys                  1: 127    2: 133   4: 141
+//   rows, 1 x 2, 513 keys                       1: 7.6    3: 8.5 (the join's launch)
+//   tile, d = 64, 272 tiles of 12001 keys       1: 224    2: 174   3: 127   4: 150
+//   tile, d = 128, 8 tiles of 20000 keys        8: 71    16: 43   32: 34
+//   tile, d = 128, 2048 tiles (causal)          1: 303    2: 456 (the partial results' traffic)
 void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
     const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv);
     int v = p->variant;
-    if (v == FC_ATTN_AUTO) v = rows > 32 ? FC_ATTN_TILE : FC_ATTN_ROWS;
-    const int64_t per = v == FC_ATTN_TILE ? 128 : (rows > 16 ? 32 : 16);
+    const int64_t cus = fc::device_cu_count();
+    if (v == FC_ATTN_AUTO) {
+        const bool full = (int64_t)s->batch * s->hkv * 2 >= cus;
+        const int64_t few = !full || s->d > 128 ? 64 : s->d > 64 ? 32 : 16;
+        v = rows <= few ? FC_ATTN_ROWS : FC_ATTN_TILE;
+    }
+    const bool tile = v == FC_ATTN_TILE;
+    const int64_t per = tile ? (s->d <= 128 ? 128 : 256) : (rows > 16 ? 32 : 16);   // rows a block
     const int64_t base = (int64_t)(s->batch > 0 ? s->batch : 1) * s->hkv * ((rows + per - 1) / per);
     const int64_t blocks = key_blocks(s, p);
-    const int64_t want = (v == FC_ATTN_TILE ? 2 : 4) * fc::device_cu_count();
-    const int64_t least = v == FC_ATTN_TILE ? 32 : 16;     // blocks of 16 keys a split at least
     int64_t n = p->splits;
     if (n == 0) {
-        n = want / base;
-        const int64_t most = (blocks + least - 1) / least;
+        // one block a CU; of the tile form as many as a CU holds
+        const int64_t want = tile ? cus * (s->d <= 64 ? 3 : s->d <= 128 ? 2 : 1) : cus;
+        n = tile ? (want + base / 2) / base : base < want ? (want + base - 1) / base : 1;
+        const int64_t most = tile ? (blocks + 31) / 32 : blocks < 64 ? 1 : (blocks + 15) / 16;
         n = n > most ? most : n;
         n = n > 256 ? 256 : n;
     }
     n = n < 1 ? 1 : n;
-    const int64_t unit = v == FC_ATTN_TILE ? 4 : 16;
-    int64_t chunk = ((blocks + n - 1) / n + unit - 1) / unit * unit;
+    const int64_t unit = tile ? 4 : 16;
+    const int64_t chunk = ((blocks + n - 1) / n + unit - 1) / unit * unit;
     if (p->splits == 0) n = (blocks + chunk - 1) / chunk;
     out->variant = v;
     out->splits = (int32_t)n;
     out->chunk = (int32_t)(chunk * 16);
-    out->workspace = n > 1 ? s->tokens * s->hq * n * (s->d + 2) * 4 : 0;
+    out->workspace = n > 1 ? s->tokens * s->hq * n * (s->d + 4) * 4 : 0;
 }
 
 }  // namespace
@@ -242,7 +262,7 @@ fc_status chain_attn(const void* q, const int64_t* strides, const uint8_t* codes
     a.out = out;
     a.lse = lse;
     a.part_o = (float*)workspace;
-    a.part_ml = p.splits > 1 ? a.part_o + shape->tokens * shape->hq * p.splits * shape->d : nullptr;
+    a.part_ml = p.splits > 1 ? (fc::floatx4*)(a.part_o + shape->tokens * shape->hq * p.splits * shape->d) : nullptr;
     a.s = kv(shape);
     a.G = shape->hq / shape->hkv;
     a.causal = params->causal != 0;

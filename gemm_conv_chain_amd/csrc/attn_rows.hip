@@ -3,16 +3,20 @@
 // k_attn_join.
 //
 // A chain of two products whose intermediate stays in registers: a wave takes
-// 64 keys at a time, S^T = K q^T (rows = keys, columns = query rows, MFMA
-// 16x16x32), the softmax of a column lives in the four lanes that hold it (the
-// running maximum and sum in 32 bits), and the weights, rounded once to the
-// activations' type, are the second product's operand B in the lanes that
-// already hold them: O^T += V^T p^T.  For that the 16 keys of accumulator rows
-// 4g .. 4g + 3 of the four tiles are the 16 tokens of one cache block: tile t,
-// row 4g + i <-> key 16g + 4t + i.
+// 64 keys (four cache blocks of 16) at a time, S^T = K q^T (rows = keys,
+// columns = query rows, MFMA 16x16x32), the softmax of a column lives in the
+// four lanes that hold it (the running maximum and sum in 32 bits), and the
+// weights, rounded once to the activations' type, become the second product's
+// operand B: O^T += V^T p^T.  Tile t is block t, so that a load of K is 1 KiB of
+// consecutive bytes; the accumulators then hold keys 4g .. 4g + 3 of block t in
+// lane group g and register t, and V's operand, 16 bytes a lane, wants block g
+// in lane group g: a transposition of 4 x 4 by eight register swaps.
 //
-// Bound by the cache's bytes: every code is read once, 16 bytes a lane, by one
-// wave.  The keys are split over a block's waves, and over blocks where
+// Bound by the cache's bytes: every code is read once, by one wave, with the
+// non-temporal hint (a plain gather of the same 16 KiB pieces: 6.1 TB/s without
+// and 7.0 with it).  K of the next keys is requested when this one's products
+// are done, V when its own are, so that a wave always has 8 to 16 KiB on the
+// way.  The keys are split over a block's waves, and over blocks where
 // sequences x heads alone do not fill the machine; the waves' results are
 // joined through LDS and the blocks' by k_attn_join, both in a fixed order.
 #include "fc_launch.h"
@@ -22,49 +26,72 @@ namespace fc {
 
 constexpr int AR_WAVES = 4;
 
-template <class T, int D, int NT, bool CAP>
-__global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row_blocks)
+__device__ __forceinline__ u32x4 load_nt(const uint8_t* p)
+{
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+}
+
+template <class T, int D, int NT, int MODE>
+__global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_attn_rows(AttnArgs a, int row_blocks)
 {
     typedef typename Tr<T>::v8 v8;
     constexpr int R = 16 * NT;       // rows a block
     constexpr int NJ = D / 64;       // 16-byte loads of K a lane and tile
     constexpr int ND = D / 16;       // tiles of V^T
     const KvShape& s = a.s;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int h = blockIdx.y / row_blocks, rb0 = blockIdx.y % row_blocks, split = blockIdx.x;
+    const int h = blockIdx.y / row_blocks, rb0 = blockIdx.y % row_blocks, split = blockIdx.z;
 
-    extern __shared__ __align__(16) float lds[];
+    extern __shared__ __align__(16) float lds[];   // [wave][NT][ND][lane] of four, then [wave][NT][16] of four
+    FC_LDS floatx4* const lds_o = (FC_LDS floatx4*)(FC_LDS float*)lds;
+    FC_LDS floatx4* const lds_ml = lds_o + AR_WAVES * NT * ND * 64;
     if constexpr (kPoison) {
-        lds_poison((FC_LDS float*)lds, 2 * NT * (D / 4 + 2) * 64 * 4, threadIdx.x, 64 * AR_WAVES);
+        lds_poison((FC_LDS float*)lds, AR_WAVES * NT * (ND * 64 + 16) * 16, threadIdx.x, 64 * AR_WAVES);
         __syncthreads();
     }
+    const NoPage* no_page = &fc_no_page;
+    asm("" : "+s"(no_page));   // the address is taken once, not by a load in every step
 
-    for (int b = blockIdx.z; b < s.batch; b += gridDim.z) {
+    {
+        const int b = blockIdx.x;
+        // The id of the first page that a lane group looks up, if the keys begin at 0: requested
+        // with the lengths rather than after them, one memory latency less before the first codes.
+        const int* const row_of = a.table + (size_t)b * s.table_stride;
+        const int first = split * a.chunk + 4 * wave + g, first_pg = first >> a.pg_shift;
+        const int raw0 = row_of[first_pg < s.table_stride ? first_pg : 0];
         long tok0;
         int nq;
         seq_range(a.cu_q, s, b, &tok0, &nq);
         const int rows = nq * a.G;
         bool over;
         const int kv_len = seq_keys(a.kv_lens, s, b, &over), pos0 = kv_len - nq;
+        const uint8_t* const head = a.codes + side_base(0, h, 0, s);
+        const size_t page_bytes = (size_t)s.hkv * 2 * s.page * D;
+        const int side_bytes = s.page * D;
         for (int r0 = rb0 * R; r0 < rows; r0 += row_blocks * R) {
             const int r1 = r0 + R < rows ? r0 + R : rows;
             const int t_first = a.by_g.div(r0), t_last = a.by_g.div(r1 - 1);
             int g_lo, g_hi;
             key_range(a, kv_len, pos0, t_first, t_last, &g_lo, &g_hi);
 
-            // this lane's rows: query, position, keys [lo, hi) that it sees
-            int hi[NT], lo[NT];
-            float slope[NT], posf[NT];
+            if (a.nsplit > 1 && g_lo + split * a.chunk >= g_hi && !over) {   // no keys for this split
+                for (int r = r0 + threadIdx.x; r < r1; r += 64 * AR_WAVES) {
+                    const int t = a.by_g.div(r), hq = h * a.G + (r - t * a.G);
+                    a.part_ml[((tok0 + t) * s.hq + hq) * a.nsplit + split] = floatx4{kNegInf, 0.0f, 0.0f, 0.0f};
+                }
+                continue;
+            }
+            // this lane's rows: position, bias, query
+            int pos[NT];
+            float slope[NT];
             v8 qf[NT][2 * NJ];
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
                 const int r = r0 + 16 * c + n, rr = r < rows ? r : rows - 1;
-                const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G), pos = pos0 + t;
-                hi[c] = a.causal ? (pos + 1 < kv_len ? pos + 1 : kv_len) : kv_len;
-                lo[c] = a.window > 0 ? pos - a.window + 1 : 0;
-                slope[c] = a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
-                posf[c] = (float)pos;
+                const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G);
+                pos[c] = pos0 + t;
+                slope[c] = MODE != SC_PLAIN && a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
                 const T* q = (const T*)a.q + (tok0 + t) * a.q_ts + (long)hq * a.q_hs;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
@@ -77,41 +104,60 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
             const int all_hi = a.causal ? (pos0 + t_first + 1 < kv_len ? pos0 + t_first + 1 : kv_len) : kv_len;
 
             floatx4 o[NT][ND];
-            float m[NT], l[NT];
+            float m[NT], l[NT], le[NT];   // maximum; sums of rounded and (for lse) of exact weights
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
                 m[c] = kNegInf;
-                l[c] = 0.0f;
+                l[c] = le[c] = 0.0f;
 #pragma unroll
                 for (int d = 0; d < ND; ++d) o[c][d] = floatx4{0, 0, 0, 0};
             }
 
             for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
                 const int c1 = c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
-                for (int k0 = c0 + 4 * wave; k0 < c1; k0 += 4 * AR_WAVES) {
-                    // the blocks of this lane: K rows of block n >> 2, scores and V of block g
-                    const int gk = k0 + (n >> 2) < c1 ? k0 + (n >> 2) : c1 - 1;
-                    const int gv = k0 + g < c1 ? k0 + g : c1 - 1;
-                    const int pk = gk >> a.pg_shift, pv = gv >> a.pg_shift;
-                    const int idk = page_id(a.table, s, b, pk), idv = page_id(a.table, s, b, pv);
-                    const uint8_t* kb = a.codes + side_base(idk < 0 ? 0 : idk, h, 0, s) + (gk - (pk << a.pg_shift)) * (16 * D) +
-                                        g * 256 + (n & 3) * 16;
-                    const uint8_t* vb = a.codes + side_base(idv < 0 ? 0 : idv, h, 1, s) + (gv - (pv << a.pg_shift)) * (16 * D) +
-                                        n * 16;
-                    u32x4 kr[4][NJ], vr[ND];
+                // Lane group g looks up block k0 + g: its page's id (two steps ahead), scales.
+                auto block_of = [&](int k0) { return k0 + g < c1 ? k0 + g : c1 - 1; };
+                auto load_id = [&](int k0) {
+                    const int pg = block_of(k0) >> a.pg_shift;
+                    const int id = row_of[pg < s.table_stride ? pg : 0];
+                    return id;
+                };
+                u32x4 kr[4][NJ], vr[ND];
+                floatx2 sc;
+                int id;      // of this lane group's block, or -1
+                auto settle_id = [&](int raw, int k0) {
+                    id = (unsigned)raw < (unsigned)s.pages && (block_of(k0) >> a.pg_shift) < s.table_stride ? raw : -1;
+                };
+                auto load_k = [&](int k0) {
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
+                    for (int t = 0; t < 4; ++t) {
+                        const int it = __builtin_amdgcn_readlane(id, 16 * t);
+                        const int kb = k0 + t < c1 ? k0 + t : c1 - 1;
+                        const uint8_t* src = it < 0 ? (const uint8_t*)no_page->codes[0]
+                                                    : head + it * page_bytes + (kb & ((1 << a.pg_shift) - 1)) * (16 * D);
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) kr[t][j] = *reinterpret_cast<const u32x4*>(kb + j * 1024 + t * 64);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) vr[d] = *reinterpret_cast<const u32x4*>(vb + d * 256);
-                    const float* sc = a.scales + ((size_t)(idv < 0 ? 0 : idv) * s.hkv + h) * 2;
-                    float ks = sc[0], vs = sc[1];
-                    if (idv < 0) {   // a page outside the pool: every row that sees its keys turns NaN
-                        ks = __builtin_nanf("");
-                        vs = 1.0f;
+                        for (int j = 0; j < NJ; ++j) kr[t][j] = load_nt(src + j * 1024 + lane * 16);
                     }
-
+                };
+                auto load_v = [&](int k0) {
+                    const uint8_t* src = id < 0 ? (const uint8_t*)no_page->codes[1]
+                                                : head + side_bytes + id * page_bytes +
+                                                      (block_of(k0) & ((1 << a.pg_shift) - 1)) * (16 * D);
+                    const float* scale = id < 0 ? no_page->scale : a.scales + ((size_t)id * s.hkv + h) * 2;
+                    sc = *reinterpret_cast<const floatx2*>(scale);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) vr[d] = load_nt(src + d * 256 + n * 16);
+                };
+                constexpr int STEP = 4 * AR_WAVES;
+                int k0 = c0 + 4 * wave;
+                if (k0 >= c1) continue;
+                // (raw0 is block k0 + g's unless that lies past the end, where its page may differ)
+                int raw = c0 == split * a.chunk && k0 + g < c1 ? raw0 : load_id(k0);
+                settle_id(raw, k0);
+                load_k(k0);
+                load_v(k0);
+                raw = load_id(k0 + STEP);
+                for (; k0 < c1; k0 += STEP) {
                     floatx4 st[NT][4];
 #pragma unroll
                     for (int t = 0; t < 4; ++t) {
@@ -126,26 +172,42 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
                                 for (int c = 0; c < NT; ++c) st[c][t] = Tr<T>::mfma16(kf, qf[c][2 * j + e], st[c][t]);
                             }
                     }
-                    const float c0s = CAP ? 2.0f * kLog2e * ks * a.scale / a.cap : ks * a.scale * kLog2e;
-                    const float c1s = a.cap * kLog2e;
-                    const int key0 = (k0 + g) * 16;
+                    const float vs = sc[1];
+                    const float f = sc[0] * (MODE == SC_ANY && a.cap > 0.0f ? 2.0f * kLog2e * a.scale / a.cap : a.scale * kLog2e);
+                    float ft[4];   // the factor of tile t's scores
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        ft[t] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), 16 * t));
+                    __builtin_amdgcn_sched_barrier(0);
+                    settle_id(raw, k0 + STEP);
+                    load_k(k0 + STEP);   // past the end: the last block again, unused
+                    __builtin_amdgcn_sched_barrier(0);
+
+                    const int key0 = k0 * 16 + 4 * g;
                     const bool masked = k0 * 16 < all_lo || (k0 + 4) * 16 > all_hi || k0 + 4 > c1;
                     v8 pf[NT][2];
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
                         float x[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = score<CAP>(st[c][i >> 2][i & 3], c0s, c1s);
-                        if (a.slopes) {
-                            const float gap = posf[c] - (float)key0;
+                        for (int i = 0; i < 16; ++i) {
+                            const float y = st[c][i >> 2][i & 3];
+                            x[i] = MODE == SC_ANY && a.cap > 0.0f ? score<true>(y, ft[i >> 2], a.cap * kLog2e) : y * ft[i >> 2];
+                        }
+                        if (MODE != SC_PLAIN) {
+                            const float gap = (float)(pos[c] - key0);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) x[i] -= slope[c] * fabsf(gap - (float)i);
+                            for (int i = 0; i < 16; ++i) x[i] -= slope[c] * fabsf(gap - (float)((i >> 2) * 16 + (i & 3)));
                         }
                         if (masked) {
-                            const int top = hi[c] < c1 * 16 ? hi[c] : c1 * 16;
+                            int top = a.causal && pos[c] + 1 < kv_len ? pos[c] + 1 : kv_len;
+                            top = (top < c1 * 16 ? top : c1 * 16) - key0;
+                            const int low = (a.window > 0 ? pos[c] - a.window + 1 : 0) - key0;
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                x[i] = key0 + i < top && key0 + i >= lo[c] ? x[i] : kNegInf;
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = (i >> 2) * 16 + (i & 3);
+                                x[i] = k < top && k >= low ? x[i] : kNegInf;
+                            }
                         }
                         float mx = x[0];
 #pragma unroll
@@ -153,26 +215,49 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
                         mx = max_x32(max_x16(mx));
                         const float mn = fmaxf(m[c], mx);
                         const float ms = mn == kNegInf ? 0.0f : mn;   // nothing seen yet: all weights are 0
-                        const float alpha = __builtin_amdgcn_exp2f(m[c] - ms);
-                        m[c] = mn;
-                        float sum = 0.0f;
-                        u32x4 w[2];
+                        if (__any(mx > m[c])) {
+                            const float alpha = __builtin_amdgcn_exp2f(m[c] - ms);
+                            m[c] = mn;
+                            l[c] *= alpha;
+                            le[c] *= alpha;
+#pragma unroll
+                            for (int d = 0; d < ND; ++d) o[c][d] *= alpha;
+                        }
+                        float sum = 0.0f, exact = 0.0f;
+                        unsigned w[4][2];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
                             const float p0 = __builtin_amdgcn_exp2f(x[i] - ms), p1 = __builtin_amdgcn_exp2f(x[i + 1] - ms);
-                            sum += p0 + p1;
-                            w[i >> 3][(i >> 1) & 3] = Tr<T>::pk(p0, p1);
+                            w[i >> 2][(i >> 1) & 1] = Tr<T>::pk(p0, p1);
+                            sum = Tr<T>::add2(w[i >> 2][(i >> 1) & 1], sum);
+                            exact += p0 + p1;
                         }
-                        l[c] = l[c] * alpha + sum;
+                        l[c] += sum;
+                        le[c] += exact;
+                        // [register t][lane group g] -> [g][t]
 #pragma unroll
-                        for (int d = 0; d < ND; ++d) o[c][d] *= alpha;
-                        pf[c][0] = __builtin_bit_cast(v8, w[0]);
-                        pf[c][1] = __builtin_bit_cast(v8, w[1]);
+                        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                const auto y = __builtin_amdgcn_permlane32_swap(w[t][e], w[t + 2][e], false, false);
+                                w[t][e] = y[0];
+                                w[t + 2][e] = y[1];
+                            }
+#pragma unroll
+                            for (int t = 0; t < 4; t += 2) {
+                                const auto y = __builtin_amdgcn_permlane16_swap(w[t][e], w[t + 1][e], false, false);
+                                w[t][e] = y[0];
+                                w[t + 1][e] = y[1];
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            pf[c][e] = __builtin_bit_cast(v8, u32x4{w[2 * e][0], w[2 * e][1], w[2 * e + 1][0], w[2 * e + 1][1]});
                     }
                     // tokens past the end hold whatever the page held: their weight is 0, and
                     // 0 times a NaN code is NaN, so their codes are cleared
-                    if ((k0 + 4) * 16 > kv_len || __any(idv < 0)) {
-                        const int keep = idv < 0 ? 0 : kv_len - key0;
+                    if ((k0 + 4) * 16 > kv_len) {
+                        const int keep = kv_len - (k0 + g) * 16;
                         u32x4 mk;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -190,76 +275,73 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
 #pragma unroll
                             for (int c = 0; c < NT; ++c) o[c][d] = Tr<T>::mfma16(vf, pf[c][e], o[c][d]);
                         }
+                    __builtin_amdgcn_sched_barrier(0);
+                    load_v(k0 + STEP);
+                    raw = load_id(k0 + 2 * STEP);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
+            // Join the waves: each brings its result to the common maximum and leaves it in LDS,
+            // and adds up, in the waves' order, a quarter of the dims.
+            __syncthreads();   // LDS is free
 #pragma unroll
-            for (int c = 0; c < NT; ++c) l[c] = over ? __builtin_nanf("") : sum_x32(sum_x16(l[c]));
-
-            // join the waves: waves 2, 3 hand theirs to 0, 1, then 1 to 0
-            constexpr int PW = NT * (ND * 4 + 2) * 64;   // floats a wave hands over
-#pragma unroll
-            for (int half = AR_WAVES / 2; half; half >>= 1) {
-                __syncthreads();
-                if (wave >= half && wave < 2 * half) {
-                    float* w = lds + (wave - half) * PW + lane;
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        w[(c * 2) * 64] = m[c];
-                        w[(c * 2 + 1) * 64] = l[c];
-#pragma unroll
-                        for (int d = 0; d < ND; ++d)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) w[(NT * 2 + (c * ND + d) * 4 + i) * 64] = o[c][d][i];
-                    }
-                }
-                __syncthreads();
-                if (wave < half) {
-                    const float* w = lds + wave * PW + lane;
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const float m2 = w[(c * 2) * 64], l2 = w[(c * 2 + 1) * 64];
-                        const float mn = fmaxf(m[c], m2), ms = mn == kNegInf ? 0.0f : mn;
-                        const float f1 = __builtin_amdgcn_exp2f(m[c] - ms), f2 = __builtin_amdgcn_exp2f(m2 - ms);
-                        m[c] = mn;
-                        l[c] = l[c] * f1 + l2 * f2;
-#pragma unroll
-                        for (int d = 0; d < ND; ++d)
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                o[c][d][i] = o[c][d][i] * f1 + w[(NT * 2 + (c * ND + d) * 4 + i) * 64] * f2;
-                    }
-                }
+            for (int c = 0; c < NT; ++c) {
+                l[c] = sum_x32(sum_x16(l[c]));
+                le[c] = sum_x32(sum_x16(le[c]));
+                if (g == 0) lds_ml[(wave * NT + c) * 16 + n] = floatx4{m[c], l[c], le[c], 0.0f};
             }
-            if (wave == 0) {
+            __syncthreads();
+            float inv[NT];
 #pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    const int r = r0 + 16 * c + n;
-                    if (r >= rows) continue;
-                    const int t = a.by_g.div(r), hq = h * a.G + (r - t * a.G);
-                    const long row = (tok0 + t) * s.hq + hq;
+            for (int c = 0; c < NT; ++c) {
+                floatx4 ml[AR_WAVES];
+                float top = kNegInf;
+#pragma unroll
+                for (int w = 0; w < AR_WAVES; ++w) {
+                    ml[w] = lds_ml[(w * NT + c) * 16 + n];
+                    top = fmaxf(top, ml[w][0]);
+                }
+                const float ms = top == kNegInf ? 0.0f : top;
+                l[c] = le[c] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < AR_WAVES; ++w) {
+                    const float f = __builtin_amdgcn_exp2f(ml[w][0] - ms);
+                    l[c] += ml[w][1] * f;
+                    le[c] += ml[w][2] * f;
+                }
+                if (over) l[c] = le[c] = __builtin_nanf("");
+                const float f = __builtin_amdgcn_exp2f(m[c] - ms);
+                m[c] = top;
+                inv[c] = a.nsplit > 1 ? 1.0f : l[c] != 0.0f ? 1.0f / l[c] : 0.0f;   // no key seen: 0
+#pragma unroll
+                for (int d = 0; d < ND; ++d) lds_o[((wave * NT + c) * ND + d) * 64 + lane] = o[c][d] * f;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int r = r0 + 16 * c + n;
+                if (r >= rows) continue;
+                const int t = a.by_g.div(r), hq = h * a.G + (r - t * a.G);
+                const long row = (tok0 + t) * s.hq + hq, at = row * a.nsplit + split;
+#pragma unroll
+                for (int dd = 0; dd < ND / AR_WAVES; ++dd) {
+                    const int d = wave * (ND / AR_WAVES) + dd;
+                    floatx4 y = lds_o[(c * ND + d) * 64 + lane];
+#pragma unroll
+                    for (int w = 1; w < AR_WAVES; ++w) y += lds_o[((w * NT + c) * ND + d) * 64 + lane];
+                    if (over) y = floatx4{l[c], l[c], l[c], l[c]};
                     if (a.nsplit == 1) {
-                        const float inv = l[c] != 0.0f ? 1.0f / l[c] : 0.0f;   // no key seen: 0
-                        T* out = (T*)a.out + row * D;
-#pragma unroll
-                        for (int d = 0; d < ND; ++d) {
-                            u32x2 w;
-                            w[0] = Tr<T>::pk(o[c][d][0] * inv, o[c][d][1] * inv);
-                            w[1] = Tr<T>::pk(o[c][d][2] * inv, o[c][d][3] * inv);
-                            *reinterpret_cast<u32x2*>(out + 16 * d + 4 * g) = w;
-                        }
-                        if (a.lse && g == 0) a.lse[row] = (m[c] + __builtin_amdgcn_logf(l[c])) * (1.0f / kLog2e);
-                    } else {
-                        const long at = row * a.nsplit + split;
-                        if (l[c] != 0.0f) {
-#pragma unroll
-                            for (int d = 0; d < ND; ++d)
-                                *reinterpret_cast<floatx4*>(a.part_o + at * D + 16 * d + 4 * g) = o[c][d];
-                        }
-                        if (g == 0) {
-                            a.part_ml[at * 2] = m[c];
-                            a.part_ml[at * 2 + 1] = l[c];
-                        }
+                        u32x2 w;
+                        w[0] = Tr<T>::pk(y[0] * inv[c], y[1] * inv[c]);
+                        w[1] = Tr<T>::pk(y[2] * inv[c], y[3] * inv[c]);
+                        *reinterpret_cast<u32x2*>((T*)a.out + row * D + 16 * d + 4 * g) = w;
+                    } else if (l[c] != 0.0f) {
+                        *reinterpret_cast<floatx4*>(a.part_o + at * D + 16 * d + 4 * g) = y;
                     }
+                }
+                if (wave == 0 && g == 0) {
+                    if (a.nsplit > 1) a.part_ml[at] = floatx4{m[c], l[c], le[c], 0.0f};
+                    else if (a.lse) a.lse[row] = (m[c] + __builtin_amdgcn_logf(le[c])) * (1.0f / kLog2e);
                 }
             }
         }
@@ -272,24 +354,25 @@ __global__ __launch_bounds__(64 * AR_WAVES) void k_attn_rows(AttnArgs a, int row
 template <class T, int WPR>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 {
-    __shared__ float part[WPR > 1 ? WPR - 1 : 1][5][64];
+    __shared__ float part[WPR > 1 ? WPR - 1 : 1][6][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % WPR, D = a.s.d;
     const long row = (long)blockIdx.x * (4 / WPR) + wave / WPR;
     const bool live = row < rows;
-    const floatx2* ml = reinterpret_cast<const floatx2*>(a.part_ml) + (live ? row : 0) * a.nsplit;
+    const floatx4* ml = a.part_ml + (live ? row : 0) * a.nsplit;
     float m = kNegInf;
     for (int k = lane; k < a.nsplit; k += 64) m = fmaxf(m, ml[k][0]);
 #pragma unroll
     for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
     const float ms = m == kNegInf ? 0.0f : m;
-    float l = 0.0f, o[4] = {0, 0, 0, 0};
+    float l = 0.0f, le = 0.0f, o[4] = {0, 0, 0, 0};
     const float* p = a.part_o + (live ? row : 0) * a.nsplit * D + lane;
 #pragma unroll 4
     for (int k = w; k < a.nsplit; k += WPR) {
-        const floatx2 v = ml[k];
+        const floatx4 v = ml[k];
         const float f = __builtin_amdgcn_exp2f(v[0] - ms);
         const bool some = v[1] != 0.0f;
         l += some ? v[1] * f : 0.0f;
+        le += some ? v[2] * f : 0.0f;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i * 64 < D) {
@@ -302,6 +385,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 #pragma unroll
             for (int i = 0; i < 4; ++i) part[w - 1][i][lane] = o[i];
             part[w - 1][4][lane] = l;
+            part[w - 1][5][lane] = le;
         }
         __syncthreads();
         if (w > 0) return;
@@ -310,6 +394,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] += part[j][i][lane];
             l += part[j][4][lane];
+            le += part[j][5][lane];
         }
     }
     if (!live) return;
@@ -318,30 +403,39 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (i * 64 < D) out[i * 64 + lane] = (T)(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[row] = (m + __builtin_amdgcn_logf(l)) * (1.0f / kLog2e);
+    if (a.lse && lane == 0) a.lse[row] = (m + __builtin_amdgcn_logf(le)) * (1.0f / kLog2e);
 }
 
-template <class T, int D, int NT, bool CAP>
+template <class T, int D, int NT, int MODE>
 static hipError_t launch_rows(const AttnArgs& a, hipStream_t st)
 {
     static std::atomic<unsigned long long> done{0};
-    const int lds = 2 * NT * (D / 4 + 2) * 64 * 4;
-    hipError_t e = allow_full_lds((const void*)k_attn_rows<T, D, NT, CAP>, &done);
+    const int lds = AR_WAVES * NT * (D / 16 * 64 + 16) * 16;
+    hipError_t e = allow_full_lds((const void*)k_attn_rows<T, D, NT, MODE>, &done);
     if (e != hipSuccess) return e;
     const long rows = (long)(a.s.max_q > 0 ? a.s.max_q : 1) * a.G;
     long rb = (rows + 16 * NT - 1) / (16 * NT);
     if (rb * a.s.hkv > 65535) rb = 65535 / a.s.hkv;
-    const dim3 grid(a.nsplit, (unsigned)(rb * a.s.hkv), a.s.batch < 65535 ? a.s.batch : 65535);
-    k_attn_rows<T, D, NT, CAP><<<grid, dim3(64 * AR_WAVES), lds, st>>>(a, (int)rb);
+    // Sequences fastest, splits slowest: workgroups go round-robin over the 8 XCDs, and with the
+    // splits fastest a power of two of them put the later ones, which only long sequences have,
+    // on the same XCDs (256 sequences of 170 - 500 keys, 8 splits: 121 us, against 52 with 6).
+    const dim3 grid(a.s.batch, (unsigned)(rb * a.s.hkv), a.nsplit);
+    k_attn_rows<T, D, NT, MODE><<<grid, dim3(64 * AR_WAVES), lds, st>>>(a, (int)rb);
     return hipGetLastError();
+}
+
+template <class T, int D, int MODE>
+static hipError_t rows_tiles(const AttnArgs& a, hipStream_t st)
+{
+    return (long)a.s.max_q * a.G > 16 ? launch_rows<T, D, 2, MODE>(a, st) : launch_rows<T, D, 1, MODE>(a, st);
 }
 
 template <class T, int D>
 static hipError_t pick_rows(const AttnArgs& a, hipStream_t st)
 {
-    const bool two = (long)a.s.max_q * a.G > 16;
-    if (a.cap > 0.0f) return two ? launch_rows<T, D, 2, true>(a, st) : launch_rows<T, D, 1, true>(a, st);
-    return two ? launch_rows<T, D, 2, false>(a, st) : launch_rows<T, D, 1, false>(a, st);
+    const int kind = score_kind(a);
+    if (kind == SC_ANY) return rows_tiles<T, D, SC_ANY>(a, st);
+    return kind == SC_BIAS ? rows_tiles<T, D, SC_BIAS>(a, st) : rows_tiles<T, D, SC_PLAIN>(a, st);
 }
 
 template <class T>

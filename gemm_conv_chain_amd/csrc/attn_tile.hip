@@ -22,25 +22,6 @@ namespace fc {
 
 typedef FC_LDS uint8_t lds_u8;
 
-// Scores of the first kind: scale * q . k alone; with a bias by distance; capped
-// (with or without a bias), or not causal with one.
-enum { SC_PLAIN = 0, SC_BIAS = 1, SC_ANY = 2 };
-
-// What a page outside the pool is read as: NaN keys, so that the rows that see
-// them turn NaN and no others, and zero values.
-struct NoPage {
-    unsigned codes[2][1024];
-    float scale[2];
-};
-__host__ __device__ constexpr NoPage make_no_page()
-{
-    NoPage p{};
-    for (int i = 0; i < 1024; ++i) p.codes[0][i] = 0x7f7f7f7fu;
-    p.scale[0] = p.scale[1] = 1.0f;
-    return p;
-}
-static __device__ __align__(16) NoPage fc_no_page = make_no_page();
-
 // Waves a block and blocks of 16 keys a stage.  Heads of 192 and 256 leave a SIMD
 // room for two waves only if a block of eight shares the widening (d = 192: 220
 // us, against 401 with four waves of 512 registers, for two prompts of 4096 and
@@ -64,8 +45,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
     const KvShape& s = a.s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
-    const int h = blockIdx.x, split = blockIdx.y % a.nsplit;
-    const int rt0 = row_tiles - 1 - (int)(blockIdx.y / a.nsplit);   // long rows (causal) first
+    const int h = blockIdx.x, split = blockIdx.y / row_tiles;
+    const int rt0 = row_tiles - 1 - (int)(blockIdx.y % row_tiles);   // long rows (causal) first
 
     extern __shared__ __align__(16) uint8_t buf[];
     lds_u8* const lb = (lds_u8*)buf;
@@ -123,7 +104,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
             floatx16 o[ND];
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] = zero16();
-            float m = kNegInf, mb = 0.0f, l = 0.0f;   // the maximum that weights refer to; with 0 for -inf
+            float m = kNegInf, mb = 0.0f;   // the maximum that weights refer to; with 0 for -inf
+            float l = 0.0f, le = 0.0f;      // sums of rounded and (for lse) of exact weights
 
             for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
                 const int c1 = c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
@@ -270,10 +252,17 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                         m = mn;
                         mb = to;
                         l *= alpha;
+                        le *= alpha;
 #pragma unroll
                         for (int d = 0; d < ND; ++d) o[d] *= alpha;
 #pragma unroll
                         for (int i = 0; i < 16 * U; ++i) x[i >> 4][i & 15] -= by;
+                    }
+                    if (a.lse) {   // (their weights once more, rather than a sum that other calls pay for)
+                        float exact = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 16 * U; ++i) exact += __builtin_amdgcn_exp2f(x[i >> 4][i & 15] * unit);
+                        le += exact;
                     }
                     // weights and second product by turns: the products with 8 keys' weights, and
                     // between them the weights of the next 8
@@ -282,8 +271,8 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                     auto weigh = [&](int i) {
                         const float p0 = __builtin_amdgcn_exp2f(x[i >> 3][2 * (i & 7)] * unit);
                         const float p1 = __builtin_amdgcn_exp2f(x[i >> 3][2 * (i & 7) + 1] * unit);
-                        sum += p0 + p1;
                         w[i >> 2][i & 3] = Tr<T>::pk(p0, p1);
+                        sum = Tr<T>::add2(w[i >> 2][i & 3], sum);
                     };
 #pragma unroll
                     for (int i = 0; i < 4; ++i) weigh(i);
@@ -301,6 +290,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                 }
             }
             l = over ? __builtin_nanf("") : sum_x32(l);
+            le = over ? l : sum_x32(le);
             if (r < rows) {
                 const long row = (tok0 + t) * s.hq + hq;
                 if (a.nsplit == 1) {
@@ -315,7 +305,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                             v[1] = Tr<T>::pk(o[d][4 * k + 2] * inv, o[d][4 * k + 3] * inv);
                             *reinterpret_cast<u32x2*>(out + 32 * d + 8 * k) = v;
                         }
-                    if (a.lse && hf == 0) a.lse[row] = (m * unit + __builtin_amdgcn_logf(l)) * (1.0f / kLog2e);
+                    if (a.lse && hf == 0) a.lse[row] = (m * unit + __builtin_amdgcn_logf(le)) * (1.0f / kLog2e);
                 } else {
                     const long at = row * a.nsplit + split;
                     if (l != 0.0f) {
@@ -327,10 +317,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                                 *reinterpret_cast<floatx4*>(out + 32 * d + 8 * k) =
                                     floatx4{o[d][4 * k], o[d][4 * k + 1], o[d][4 * k + 2], o[d][4 * k + 3]};
                     }
-                    if (hf == 0) {
-                        a.part_ml[at * 2] = m * unit;
-                        a.part_ml[at * 2 + 1] = l;
-                    }
+                    if (hf == 0) a.part_ml[at] = floatx4{m * unit, l, le, 0.0f};
                 }
             }
         }
@@ -357,8 +344,9 @@ static hipError_t launch_tile(const AttnArgs& a, hipStream_t st)
 template <class T, int D>
 static hipError_t tile_mode(const AttnArgs& a, hipStream_t st)
 {
-    if (a.cap > 0.0f || (a.slopes && !a.causal)) return launch_tile<T, D, SC_ANY>(a, st);
-    return a.slopes ? launch_tile<T, D, SC_BIAS>(a, st) : launch_tile<T, D, SC_PLAIN>(a, st);
+    const int kind = score_kind(a);
+    if (kind == SC_ANY) return launch_tile<T, D, SC_ANY>(a, st);
+    return kind == SC_BIAS ? launch_tile<T, D, SC_BIAS>(a, st) : launch_tile<T, D, SC_PLAIN>(a, st);
 }
 
 template <class T>

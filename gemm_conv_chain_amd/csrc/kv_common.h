@@ -55,6 +55,13 @@ template <> struct Tr<half_t> {
         h[1] = (half_t)b;
         return __builtin_bit_cast(unsigned, h);
     }
+    // s + the two values of w, in 32 bits
+    __device__ static __forceinline__ float add2(unsigned w, float s)
+    {
+        half2v one;
+        one[0] = one[1] = (half_t)1.0f;
+        return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2v, w), one, s, false);
+    }
     __device__ static __forceinline__ floatx4 mfma16(v8 a, v8 b, floatx4 c)
     {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -78,6 +85,12 @@ template <> struct Tr<bf16_t> {
         h[0] = (bf16_t)a;
         h[1] = (bf16_t)b;
         return __builtin_bit_cast(unsigned, h);
+    }
+    __device__ static __forceinline__ float add2(unsigned w, float s)
+    {
+        bf2 one;
+        one[0] = one[1] = (bf16_t)1.0f;
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2, w), one, s, false);
     }
     __device__ static __forceinline__ floatx4 mfma16(v8 a, v8 b, floatx4 c)
     {
@@ -259,7 +272,8 @@ struct AttnArgs {
     const float* slopes;   // [hq] or NULL
     void* out;             // [tokens, hq, d]
     float* lse;            // [tokens, hq] or NULL
-    float *part_o, *part_ml;   // workspace of nsplit > 1: [tokens, hq, nsplit, d] and [.., 2]
+    float* part_o;         // workspace of nsplit > 1: [tokens, hq, nsplit, d] and
+    floatx4* part_ml;      // [tokens, hq, nsplit] of {maximum (log 2), sum of weights, exact sum (for lse), -}
     KvShape s;
     int G, causal, window, nsplit, chunk;   // chunk: blocks of 16 keys a split
     int pg_shift;                            // a page holds 2^pg_shift blocks of 16
@@ -278,6 +292,34 @@ __device__ __forceinline__ void key_range(const AttnArgs& a, int kv_len, int pos
     *g0 = lo >> 4;
     *g1 = hi > lo ? (hi + 15) >> 4 : *g0;
 }
+
+// What a page outside the pool is read as: NaN keys, so that the rows that see
+// them turn NaN and no others, and zero values.
+struct NoPage {
+    unsigned codes[2][1024];   // the 4 KiB of a block of 16 tokens, d = 256
+    float scale[2];
+};
+__host__ __device__ constexpr NoPage make_no_page()
+{
+    NoPage p{};
+    for (int i = 0; i < 1024; ++i) p.codes[0][i] = 0x7f7f7f7fu;
+    p.scale[0] = p.scale[1] = 1.0f;
+    return p;
+}
+static __device__ __align__(16) NoPage fc_no_page = make_no_page();
+
+// Scores of the plain kind: scale * q . k alone; with a bias by distance; capped
+// (with or without a bias), or not causal with one.
+enum { SC_PLAIN = 0, SC_BIAS = 1, SC_ANY = 2 };
+inline int score_kind(const AttnArgs& a)
+{
+    return a.cap > 0.0f || (a.slopes && !a.causal) ? SC_ANY : a.slopes ? SC_BIAS : SC_PLAIN;
+}
+
+// The weights are rounded to the activations' type before the second product.
+// The sum that divides the result is of the rounded ones, so that it matches its
+// numerator (a row of one dominant key comes out as that key's value); the sum
+// of the unrounded ones is only kept where lse is asked for.
 
 // Score modification, in units of log 2: s is q . k on the codes.  Without a
 // cap c0 = k scale * softmax scale * log2 e; with one c0 = 2 log2 e * k scale *
