@@ -115,6 +115,14 @@ __device__ __forceinline__ typename Tr<T>::v8 frag8(unsigned w0, unsigned w1, fl
 }
 
 template <class T>
+__device__ __forceinline__ void unpack8(u32x4 w, float (&x)[8])
+{
+    const typename Tr<T>::v8 v = __builtin_bit_cast(typename Tr<T>::v8, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
+}
+
+template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&x)[8])
 {
     const typename Tr<T>::v8 v = *reinterpret_cast<const typename Tr<T>::v8*>(p);
@@ -230,6 +238,38 @@ __device__ __forceinline__ void unit_angles(const unsigned long long* turns, int
         turn_sincos(p, turns[u * 8 + j], sn[j], cs[j]);
         cs[j] *= mscale;
         sn[j] *= mscale * sign;
+    }
+}
+
+// One unit of up to HPT heads, whose angles are computed once: p + k * ph to o +
+// k * oh.  The loads go out together and stay packed until their head's turn, so
+// that registers leave room for waves (p and o may be the same).
+template <class T, int HPT>
+__device__ __forceinline__ void turn_heads(const T* p, T* o, long ph, long oh, const Unit& at, const RopeArgs& r, int u, int pos,
+                                           float sign, int heads)
+{
+    u32x4 w[HPT][2];
+#pragma unroll
+    for (int k = 0; k < HPT; ++k) {
+        if (HPT > 1 && k >= heads) break;
+        w[k][0] = *reinterpret_cast<const u32x4*>(p + k * ph + at.e0);
+        w[k][1] = *reinterpret_cast<const u32x4*>(p + k * ph + at.e1);
+    }
+    float cs[8], sn[8];
+    if (at.turned) unit_angles(r.turns, u, pos, r.mscale, sign, cs, sn);
+#pragma unroll
+    for (int k = 0; k < HPT; ++k) {
+        if (HPT > 1 && k >= heads) break;
+        if (at.turned) {
+            float x0[8], x1[8];
+            unpack8<T>(w[k][0], x0);
+            unpack8<T>(w[k][1], x1);
+            rotate_unit(x0, x1, cs, sn, r.interleaved);
+            w[k][0] = pack8<T>(x0);
+            w[k][1] = pack8<T>(x1);
+        }
+        *reinterpret_cast<u32x4*>(o + k * oh + at.e0) = w[k][0];
+        *reinterpret_cast<u32x4*>(o + k * oh + at.e1) = w[k][1];
     }
 }
 

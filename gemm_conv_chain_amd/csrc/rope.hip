@@ -27,25 +27,7 @@ __global__ __launch_bounds__(256) void k_rope(const T* x, T* y, long xt, long xh
     const int h0 = hb * HPT;
     const T* px = x + (long)t * xt + (long)h0 * xh;
     T* py = y + (long)t * yt + (long)h0 * yh;
-    float x0[HPT][8], x1[HPT][8];
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        if (HPT > 1 && h0 + k >= heads) break;
-        load8(px + k * xh + at.e0, x0[k]);
-        load8(px + k * xh + at.e1, x1[k]);
-    }
-    if (at.turned) {
-        float cs[8], sn[8];
-        unit_angles(r.turns, u, positions[t], r.mscale, sign, cs, sn);
-#pragma unroll
-        for (int k = 0; k < HPT; ++k) rotate_unit(x0[k], x1[k], cs, sn, r.interleaved);
-    }
-#pragma unroll
-    for (int k = 0; k < HPT; ++k) {
-        if (HPT > 1 && h0 + k >= heads) break;
-        *reinterpret_cast<u32x4*>(py + k * yh + at.e0) = pack8<T>(x0[k]);
-        *reinterpret_cast<u32x4*>(py + k * yh + at.e1) = pack8<T>(x1[k]);
-    }
+    turn_heads<T, HPT>(px, py, xh, yh, at, r, u, at.turned ? positions[t] : 0, sign, heads - h0);
 }
 
 template <class T, int HPT>
