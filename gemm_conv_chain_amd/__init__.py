@@ -785,39 +785,59 @@ def pad_weight_channels(w, c_out):
 
 
 # ---------------------------------------- attention over a paged 8-bit cache
+# These calls are made for every layer of every step, so their checks are few
+# and plain: a launch of 3 us should not wait for 10 us of checking.
 _STRIDES = {n: _i64 * n for n in (2, 4, 6)}
+
+
+_CODES = {}   # torch dtype -> fc_dtype
 
 
 def _rows(t, name, dtype=None):
     """t [tokens, heads, d] of a 16-bit float type, elements of a head adjacent;
     token and head strides are free.  Returns its fc_dtype."""
-    torch = _torch()
-    if len(_ndim(t, name, 3)) != 3:
-        raise ValueError("%s must be [tokens, heads, d]" % name)
-    if t.dtype is torch.float16:
-        code = 0
-    elif t.dtype is torch.bfloat16:
-        code = 1
-    else:
-        raise TypeError("%s must be torch.float16 or torch.bfloat16, got %s" % (name, t.dtype))
+    if not _CODES:
+        torch = _torch()
+        _CODES.update({torch.float16: 0, torch.bfloat16: 1})
+    code = _CODES.get(getattr(t, "dtype", None))
+    if code is None:
+        raise TypeError("%s must be a torch tensor of float16 or bfloat16, got %s"
+                        % (name, getattr(t, "dtype", type(t).__name__)))
     if dtype is not None and code != dtype:
         raise TypeError("%s is %s, unlike the other activations" % (name, t.dtype))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    if t.dim() != 3:
+        raise ValueError("%s must be [tokens, heads, d], got shape %s" % (name, tuple(t.shape)))
+    if t.stride(2) != 1 and t.shape[2] > 1:
         raise ValueError("the elements of a head of %s must be adjacent" % name)
     return code
 
 
-def _same_device(items):
-    dev = None
-    for t, name in items:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise TypeError("%s must be a device tensor" % name)
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, dev))
+def _exact(t, name, shape, dtype):
+    """t is a contiguous torch tensor of this shape and type."""
+    if getattr(t, "dtype", None) is not dtype:
+        raise TypeError("%s must be a torch tensor of %s, got %s" % (name, dtype, getattr(t, "dtype", type(t).__name__)))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _one_device(dev, tensors):
+    """Every tensor (None: absent) sits on device `dev`."""
+    if dev < 0:
+        raise TypeError("the activations must be device tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            if t.is_cuda:
+                raise ValueError("a tensor of shape %s is on %s, the activations on device %d" % (tuple(t.shape), t.device, dev))
+            raise TypeError("a tensor of shape %s is no device tensor, the activations are" % (tuple(t.shape),))
+
+
+def _raw_stream(dev):
+    """torch's current stream of device `dev`."""
+    return _torch()._C._cuda_getCurrentRawStream(dev)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=4.0, device=None):
@@ -872,11 +892,10 @@ def _table(turns, interleaved, mscale):
     torch = _torch()
     if turns is None:
         return None
-    _ndim(turns, "turns", 1)
-    if turns.dtype is not torch.int64:
-        raise TypeError("turns must be torch.int64, got %s" % turns.dtype)
-    if not turns.is_contiguous():
-        raise ValueError("turns must be contiguous")
+    if not isinstance(turns, torch.Tensor) or turns.dtype is not torch.int64:
+        raise TypeError("turns must be a tensor of torch.int64")
+    if turns.dim() != 1 or not turns.is_contiguous():
+        raise ValueError("turns must be contiguous with one dim, got shape %s" % (tuple(turns.shape),))
     return RopeTable(turns.data_ptr(), 2 * turns.shape[0], 1 if interleaved else 0, mscale)
 
 
@@ -886,25 +905,24 @@ def rope(x, positions, turns, interleaved=False, mscale=1.0, inverse=False, out=
     rot / 2), or (2 i, 2 i + 1) if ``interleaved``.  ``inverse`` turns back, which is
     also the gradient.  ``out`` may be x itself."""
     dt = _rows(x, "x")
-    T, H, D = x.shape
+    T, H, D = shape = x.shape
     table = _table(turns, interleaved, mscale)
     if table is None:
         raise ValueError("turns is required")
-    _ndim(positions, "positions", 1)
-    if positions.dtype is not _torch().int32:
-        raise TypeError("positions must be torch.int32, got %s" % positions.dtype)
-    if positions.shape[0] != T or not positions.is_contiguous():
-        raise ValueError("positions must be contiguous with shape (%d,), got %s" % (T, tuple(positions.shape)))
+    _exact(positions, "positions", (T,), _torch().int32)
+    if out is not None:
+        _rows(out, "out", dt)
+        if out.shape != shape:
+            raise ValueError("out must have shape %s, got %s" % (tuple(shape), tuple(out.shape)))
+    dev = x.get_device()
+    _one_device(dev, (positions, turns, out))
     if out is None:
-        _same_device(((x, "x"), (positions, "positions"), (turns, "turns")))
-        out = _empty((T, H, D), x)
-    else:
-        if _rows(out, "out", dt) is not None and tuple(out.shape) != (T, H, D):
-            raise ValueError("out must have shape %s, got %s" % ((T, H, D), tuple(out.shape)))
-        _same_device(((x, "x"), (positions, "positions"), (turns, "turns"), (out, "out")))
+        out = x.new_empty(shape)
     st = _STRIDES[4](x.stride(0), x.stride(1), out.stride(0), out.stride(1))
-    _check("rope", lib().rope_apply(_ptr(x), _ptr(out), st, _ptr(positions), table, 1 if inverse else 0, dt, T, H, D,
-                                    _stream(x)))
+    s = lib().rope_apply(x.data_ptr(), out.data_ptr(), st, positions.data_ptr(), table, 1 if inverse else 0, dt, T, H, D,
+                         _raw_stream(dev))
+    if s:
+        _check("rope", s)
     return out
 
 
@@ -921,21 +939,17 @@ def kv_cache(pages, hkv, page, d, device="cuda"):
 def _kv_shape(dt, tokens, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv):
     """Checks the cache's and the batch's tensors against each other."""
     torch = _torch()
-    P, H, two, n, w = _ndim(codes, "codes", 5)
-    if (H, two, w) != (hkv, 2, 16 * d):
+    if len(_ndim(codes, "codes", 5)) == 5:
+        _exact(codes, "codes", codes.shape, torch.uint8)
+    P, H, two, n, w = codes.shape
+    if H != hkv or two != 2 or w != 16 * d:
         raise ValueError("codes must have shape (pages, %d, 2, page / 16, %d), got %s" % (hkv, 16 * d, tuple(codes.shape)))
-    B, stride = _ndim(table, "table", 2)
-    for t, name, shape, dtype in ((codes, "codes", None, torch.uint8), (scales, "scales", (P, H, 2), torch.float32),
-                                  (table, "table", None, torch.int32), (cu_q, "cu_q", (B + 1,), torch.int32),
-                                  (kv_lens, "kv_lens", (B,), torch.int32)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s must be a torch tensor, got %s" % (name, type(t).__name__))
-        if t.dtype is not dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-        if shape is not None and tuple(t.shape) != shape:
-            raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-        if not t.is_contiguous():
-            raise ValueError("%s must be contiguous" % name)
+    B, stride = shape = _ndim(table, "table", 2)
+    i32 = torch.int32
+    _exact(scales, "scales", (P, H, 2), torch.float32)
+    _exact(table, "table", shape, i32)
+    _exact(cu_q, "cu_q", (B + 1,), i32)
+    _exact(kv_lens, "kv_lens", (B,), i32)
     page = 16 * n
     return KvShape(dt, B, hq, hkv, d, page, P, stride, tokens, tokens if max_q is None else int(max_q),
                    min(stride * page, 0x7fffffff) if max_kv is None else int(max_kv))
@@ -954,34 +968,30 @@ def kv_append(k, v, codes, scales, table, cu_q, kv_lens, turns=None, interleaved
     T, hkv, d = k.shape
     if v.shape != k.shape:
         raise ValueError("v must have k's shape %s, got %s" % (tuple(k.shape), tuple(v.shape)))
-    hq = hkv
+    hq, qs = hkv, (0, 0)
     if q is not None:
         _rows(q, "q", dt)
-        if q.shape[0] != T or q.shape[2] != d:
+        Tq, hq, dq = q.shape
+        if Tq != T or dq != d:
             raise ValueError("q must have shape (%d, hq, %d), got %s" % (T, d, tuple(q.shape)))
-        hq = q.shape[1]
+        qs = q.stride()
+        if q_out is not None:
+            _exact(q_out, "q_out", q.shape, q.dtype)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, None)
     rt = _table(turns, interleaved, mscale)
     if positions is not None:
-        _ndim(positions, "positions", 1)
-        if positions.dtype is not _torch().int32:
-            raise TypeError("positions must be torch.int32, got %s" % positions.dtype)
-        if positions.shape[0] != T or not positions.is_contiguous():
-            raise ValueError("positions must be contiguous with shape (%d,), got %s" % (T, tuple(positions.shape)))
-    if q_out is not None:
-        _rows(q_out, "q_out", dt)
-        if q_out.shape != q.shape or not q_out.is_contiguous():
-            raise ValueError("q_out must be contiguous with shape %s, got %s" % (tuple(q.shape), tuple(q_out.shape)))
-    _same_device(((k, "k"), (v, "v"), (q, "q"), (q_out, "q_out"), (codes, "codes"), (scales, "scales"),
-                  (table, "table"), (cu_q, "cu_q"), (kv_lens, "kv_lens"), (positions, "positions"), (turns, "turns")))
+        _exact(positions, "positions", (T,), _torch().int32)
+    dev = k.get_device()
+    _one_device(dev, (v, q, q_out, codes, scales, table, cu_q, kv_lens, positions, turns))
     if q is not None and q_out is None:
-        q_out = _empty((T, hq, d), q)
-    qs = (0, 0) if q is None else (q.stride(0), q.stride(1))
-    st = _STRIDES[6](k.stride(0), k.stride(1), v.stride(0), v.stride(1), *qs)
-    _check("kv_append", lib().kv_append(_ptr(k), _ptr(v), _ptr(q), _ptr(q_out), st, _ptr(codes), _ptr(scales),
-                                        _ptr(table), _ptr(cu_q), _ptr(kv_lens), _ptr(positions), rt, sh, _stream(k)))
+        q_out = q.new_empty(q.shape)
+    st = _STRIDES[6](k.stride(0), k.stride(1), v.stride(0), v.stride(1), qs[0], qs[1])
+    s = lib().kv_append(k.data_ptr(), v.data_ptr(), _addr(q), _addr(q_out), st, codes.data_ptr(), scales.data_ptr(),
+                        table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), _addr(positions), rt, sh, _raw_stream(dev))
+    if s:
+        _check("kv_append", s)
     return q_out
 
 
@@ -1034,40 +1044,38 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     (allocated if None); ``variant``, ``splits``: kernel form and split, by rule if not given."""
     torch = _torch()
     dt = _rows(q, "q")
-    T, hq, d = q.shape
-    hkv = codes.shape[1] if _ndim(codes, "codes", 5) else 0
+    T, hq, d = shape = q.shape
+    hkv = _ndim(codes, "codes", 5)[1]
     sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv)
     pa = _attn_params(d, scale, causal, softcap, window, variant, splits)
-    if slopes is not None and (_ndim(slopes, "slopes", 1) != (hq,) or not slopes.is_contiguous()):
-        raise ValueError("slopes must be contiguous with shape (%d,), got %s" % (hq, tuple(slopes.shape)))
-    if slopes is not None and slopes.dtype is not torch.float32:
-        raise TypeError("slopes must be torch.float32, got %s" % slopes.dtype)
+    if slopes is not None:
+        _exact(slopes, "slopes", (hq,), torch.float32)
     if out is not None:
-        _rows(out, "out", dt)
-        if out.shape != q.shape or not out.is_contiguous():
-            raise ValueError("out must be contiguous with shape %s, got %s" % (tuple(q.shape), tuple(out.shape)))
+        _exact(out, "out", shape, q.dtype)
     le = None if lse is True or lse is False else lse
     if le is not None:
-        _ndim(le, "lse", 2)
-        if le.dtype is not torch.float32:
-            raise TypeError("lse must be torch.float32, got %s" % le.dtype)
-        if tuple(le.shape) != (T, hq) or not le.is_contiguous():
-            raise ValueError("lse must be contiguous with shape %s, got %s" % ((T, hq), tuple(le.shape)))
+        _exact(le, "lse", (T, hq), torch.float32)
     if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         raise TypeError("workspace must be contiguous torch.uint8")
-    _same_device(((q, "q"), (codes, "codes"), (scales, "scales"), (table, "table"), (cu_q, "cu_q"),
-                  (kv_lens, "kv_lens"), (slopes, "slopes"), (out, "out"), (le, "lse"), (workspace, "workspace")))
+    dev = q.get_device()
+    _one_device(dev, (codes, scales, table, cu_q, kv_lens, slopes, out, le, workspace))
     L = lib()
     plan = AttnPlan()
-    _check("chain_attn", L.chain_attn_plan(sh, pa, plan))
+    s = L.chain_attn_plan(sh, pa, plan)
+    if s:
+        _check("chain_attn", s)
     if out is None:
-        out = _empty((T, hq, d), q)
+        out = q.new_empty(shape)
     if lse is True:
-        le = _empty((T, hq), q, torch.float32)
-    if workspace is None and plan.workspace:
-        workspace = torch.empty(plan.workspace, dtype=torch.uint8, device=q.device)
-    st = _STRIDES[2](q.stride(0), q.stride(1))
-    _check("chain_attn", L.chain_attn(_ptr(q), st, _ptr(codes), _ptr(scales), _ptr(table), _ptr(cu_q), _ptr(kv_lens),
-                                      _ptr(slopes), pa, _ptr(out), _ptr(le), sh, _ptr(workspace),
-                                      0 if workspace is None else workspace.numel(), _stream(q)))
+        le = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+    room = plan.workspace
+    if workspace is not None:
+        room = workspace.numel()
+    elif room:
+        workspace = torch.empty(room, dtype=torch.uint8, device=q.device)
+    s = L.chain_attn(q.data_ptr(), _STRIDES[2](q.stride(0), q.stride(1)), codes.data_ptr(), scales.data_ptr(),
+                     table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), _addr(slopes), pa, out.data_ptr(), _addr(le), sh,
+                     _addr(workspace), room, _raw_stream(dev))
+    if s:
+        _check("chain_attn", s)
     return (out, le) if le is not None else out
