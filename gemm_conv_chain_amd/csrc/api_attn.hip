@@ -76,7 +76,8 @@ fc_status check_shape(const fc_kv_shape* s)
         return fail(FC_E_UNSUPPORTED, "d=%d: 64, 128, 192 and 256 are implemented", s->d);
     if (s->page < 16 || s->page > 256 || (s->page & (s->page - 1)))
         return fail(FC_E_UNSUPPORTED, "page=%d: 16, 32, 64, 128 and 256 are implemented", s->page);
-    // rows of a sequence and key positions are 32-bit
+    // grid sizes, rows of a sequence and key positions are 32-bit
+    if (s->batch > (1 << 20)) return fail(FC_E_UNSUPPORTED, "batch=%d exceeds 2^20", s->batch);
     if (s->hq > 65535) return fail(FC_E_UNSUPPORTED, "hq=%d exceeds 65535", s->hq);
     if (s->tokens * s->hq > 0x3fffffffL) return fail(FC_E_UNSUPPORTED, "tokens*hq exceeds 2^30 - 1");
     if ((int64_t)s->page * s->table_stride > 0x7fff0000L)
@@ -161,7 +162,7 @@ void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
         // one block a CU; of the tile form as many as a CU holds
         const int64_t want = tile ? cus * (s->d <= 64 ? 3 : s->d <= 128 ? 2 : 1) : cus;
         n = tile ? (want + base / 2) / base : base < want ? (want + base - 1) / base : 1;
-        const int64_t most = tile ? (blocks + 31) / 32 : blocks < 64 ? 1 : (blocks + 15) / 16;
+        const int64_t most = tile ? (blocks + 23) / 24 : blocks < 64 ? 1 : (blocks + 15) / 16;
         n = n > most ? most : n;
         n = n > 256 ? 256 : n;
     }

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                 const int r = r0 + 16 * c + n, rr = r < rows ? r : rows - 1;
                 const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G);
                 pos[c] = pos0 + t;
-                slope[c] = MODE != SC_PLAIN && a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
+                slope[c] = (MODE == SC_BIAS || MODE == SC_ANY) && a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
                 const T* q = (const T*)a.q + (tok0 + t) * a.q_ts + (long)hq * a.q_hs;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
@@ -103,6 +103,9 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
             const int all_lo = a.window > 0 ? pos0 + t_last - a.window + 1 : 0;
             const int all_hi = a.causal ? (pos0 + t_first + 1 < kv_len ? pos0 + t_first + 1 : kv_len) : kv_len;
 
+            // scores in units of log 2 are q . k on the codes, times the page's scale, times this
+            const bool cap = MODE == SC_CAP || (MODE == SC_ANY && a.cap > 0.0f);
+            const float factor = cap ? 2.0f * kLog2e * a.scale / a.cap : a.scale * kLog2e;
             floatx4 o[NT][ND];
             float m[NT], l[NT], le[NT];   // maximum; sums of rounded and (for lse) of exact weights
 #pragma unroll
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                             }
                     }
                     const float vs = sc[1];
-                    const float f = sc[0] * (MODE == SC_ANY && a.cap > 0.0f ? 2.0f * kLog2e * a.scale / a.cap : a.scale * kLog2e);
+                    const float f = sc[0] * factor;
                     float ft[4];   // the factor of tile t's scores
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
@@ -192,9 +195,9 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float y = st[c][i >> 2][i & 3];
-                            x[i] = MODE == SC_ANY && a.cap > 0.0f ? score<true>(y, ft[i >> 2], a.cap * kLog2e) : y * ft[i >> 2];
+                            x[i] = cap ? capped(y, ft[i >> 2], a.cap * kLog2e, 0.0f) : y * ft[i >> 2];
                         }
-                        if (MODE != SC_PLAIN) {
+                        if (MODE == SC_BIAS || MODE == SC_ANY) {
                             const float gap = (float)(pos[c] - key0);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) x[i] -= slope[c] * fabsf(gap - (float)((i >> 2) * 16 + (i & 3)));
@@ -356,54 +359,58 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs a, long rows)
 {
     __shared__ float part[WPR > 1 ? WPR - 1 : 1][6][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, w = wave % WPR, D = a.s.d;
-    const long row = (long)blockIdx.x * (4 / WPR) + wave / WPR;
-    const bool live = row < rows;
-    const floatx4* ml = a.part_ml + (live ? row : 0) * a.nsplit;
-    float m = kNegInf;
-    for (int k = lane; k < a.nsplit; k += 64) m = fmaxf(m, ml[k][0]);
+    for (long row0 = (long)blockIdx.x * (4 / WPR); row0 < rows; row0 += (long)gridDim.x * (4 / WPR)) {
+        const bool live = row0 + wave / WPR < rows;
+        const long row = live ? row0 + wave / WPR : rows - 1;
+        const floatx4* ml = a.part_ml + row * a.nsplit;
+        float m = kNegInf;
+        for (int k = lane; k < a.nsplit; k += 64) m = fmaxf(m, ml[k][0]);
 #pragma unroll
-    for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
-    const float ms = m == kNegInf ? 0.0f : m;
-    float l = 0.0f, le = 0.0f, o[4] = {0, 0, 0, 0};
-    const float* p = a.part_o + (live ? row : 0) * a.nsplit * D + lane;
+        for (int s = 32; s; s >>= 1) m = fmaxf(m, __shfl_xor(m, s));
+        const float ms = m == kNegInf ? 0.0f : m;
+        float l = 0.0f, le = 0.0f, o[4] = {0, 0, 0, 0};
+        const float* p = a.part_o + row * a.nsplit * D + lane;
 #pragma unroll 4
-    for (int k = w; k < a.nsplit; k += WPR) {
-        const floatx4 v = ml[k];
-        const float f = __builtin_amdgcn_exp2f(v[0] - ms);
-        const bool some = v[1] != 0.0f;
-        l += some ? v[1] * f : 0.0f;
-        le += some ? v[2] * f : 0.0f;
+        for (int k = w; k < a.nsplit; k += WPR) {
+            const floatx4 v = ml[k];
+            const float f = __builtin_amdgcn_exp2f(v[0] - ms);
+            const bool some = v[1] != 0.0f;
+            l += some ? v[1] * f : 0.0f;
+            le += some ? v[2] * f : 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i * 64 < D) {
+                    const float y = p[(long)k * D + i * 64] * f;
+                    o[i] += some ? y : 0.0f;
+                }
+        }
+        if (WPR > 1) {   // in the waves' order, whatever their timing
+            if (w > 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) part[w - 1][i][lane] = o[i];
+                part[w - 1][4][lane] = l;
+                part[w - 1][5][lane] = le;
+            }
+            __syncthreads();
+            if (w == 0) {
+#pragma unroll
+                for (int j = 0; j < WPR - 1; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] += part[j][i][lane];
+                    l += part[j][4][lane];
+                    le += part[j][5][lane];
+                }
+            }
+            __syncthreads();   // the shared memory is free again
+        }
+        if (!live || w > 0) continue;
+        const float inv = l != 0.0f ? 1.0f / l : 0.0f;
+        T* out = (T*)a.out + row * D;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (i * 64 < D) {
-                const float y = p[(long)k * D + i * 64] * f;
-                o[i] += some ? y : 0.0f;
-            }
+            if (i * 64 < D) out[i * 64 + lane] = (T)(o[i] * inv);
+        if (a.lse && lane == 0) a.lse[row] = (m + __builtin_amdgcn_logf(le)) * (1.0f / kLog2e);
     }
-    if (WPR > 1) {   // in the waves' order, whatever their timing
-        if (w > 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[w - 1][i][lane] = o[i];
-            part[w - 1][4][lane] = l;
-            part[w - 1][5][lane] = le;
-        }
-        __syncthreads();
-        if (w > 0) return;
-#pragma unroll
-        for (int j = 0; j < WPR - 1; ++j) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] += part[j][i][lane];
-            l += part[j][4][lane];
-            le += part[j][5][lane];
-        }
-    }
-    if (!live) return;
-    const float inv = l != 0.0f ? 1.0f / l : 0.0f;
-    T* out = (T*)a.out + row * D;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (i * 64 < D) out[i * 64 + lane] = (T)(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[row] = (m + __builtin_amdgcn_logf(le)) * (1.0f / kLog2e);
 }
 
 template <class T, int D, int NT, int MODE>
@@ -433,9 +440,7 @@ static hipError_t rows_tiles(const AttnArgs& a, hipStream_t st)
 template <class T, int D>
 static hipError_t pick_rows(const AttnArgs& a, hipStream_t st)
 {
-    const int kind = score_kind(a);
-    if (kind == SC_ANY) return rows_tiles<T, D, SC_ANY>(a, st);
-    return kind == SC_BIAS ? rows_tiles<T, D, SC_BIAS>(a, st) : rows_tiles<T, D, SC_PLAIN>(a, st);
+    return by_kind(a, [&](auto k) { return rows_tiles<T, D, decltype(k)::value>(a, st); });
 }
 
 template <class T>
@@ -459,8 +464,10 @@ template <class T>
 static hipError_t launch_join(const AttnArgs& a, hipStream_t st)
 {
     const long rows = a.s.tokens * a.s.hq;
-    if (a.nsplit > 8) k_attn_join<T, 4><<<dim3((unsigned)rows), dim3(256), 0, st>>>(a, rows);
-    else k_attn_join<T, 1><<<dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st>>>(a, rows);
+    const long blocks = a.nsplit > 8 ? rows : (rows + 3) / 4;
+    const dim3 grid((unsigned)(blocks < (1L << 20) ? blocks : 1L << 20));
+    if (a.nsplit > 8) k_attn_join<T, 4><<<grid, dim3(256), 0, st>>>(a, rows);
+    else k_attn_join<T, 1><<<grid, dim3(256), 0, st>>>(a, rows);
     return hipGetLastError();
 }
 

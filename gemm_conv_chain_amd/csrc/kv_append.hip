@@ -478,7 +478,8 @@ static hipError_t launch_append(AppendArgs a, hipStream_t st)
     const long mq = a.s.max_q > 0 ? a.s.max_q : 1;
     const long kept = (mq < a.s.page ? mq : a.s.page) * (long)a.s.d;   // keys a block turns at most
     a.lds_floats = kept <= 15360 ? (int)kept : 0;
-    a.nslots = mq == 1 ? 1 : (int)((mq + a.s.page - 2) / a.s.page + 1);
+    const long slots = mq == 1 ? 1 : (mq + a.s.page - 2) / a.s.page + 1;
+    a.nslots = (int)(slots < 65536 ? slots : 65536);   // (blocks loop)
     a.qblocks = a.q ? (int)((query_blocks(a, HPT, mq, 128L * WPS) + a.s.hkv - 1) / a.s.hkv) : 0;
     const dim3 grid((unsigned)(a.nslots + a.qblocks), a.s.hkv, a.s.batch < 65535 ? a.s.batch : 65535);
     k_kv_append<T, WPS, HPT><<<grid, dim3(128 * WPS), a.lds_floats * 4, st>>>(a);

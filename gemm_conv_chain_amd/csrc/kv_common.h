@@ -348,12 +348,23 @@ __host__ __device__ constexpr NoPage make_no_page()
 }
 static __device__ __align__(16) NoPage fc_no_page = make_no_page();
 
-// Scores of the plain kind: scale * q . k alone; with a bias by distance; capped
-// (with or without a bias), or not causal with one.
-enum { SC_PLAIN = 0, SC_BIAS = 1, SC_ANY = 2 };
+// Kinds of scores: scale * q . k alone; with a bias by distance (causal); capped;
+// everything else, a cap and a bias or a bias to both sides.
+enum { SC_PLAIN = 0, SC_BIAS = 1, SC_CAP = 2, SC_ANY = 3 };
 inline int score_kind(const AttnArgs& a)
 {
-    return a.cap > 0.0f || (a.slopes && !a.causal) ? SC_ANY : a.slopes ? SC_BIAS : SC_PLAIN;
+    if (!a.slopes) return a.cap > 0.0f ? SC_CAP : SC_PLAIN;
+    return a.cap > 0.0f || !a.causal ? SC_ANY : SC_BIAS;
+}
+// Calls f(IntC<kind>{}) for the call's kind.
+template <class F> inline hipError_t by_kind(const AttnArgs& a, F&& f)
+{
+    switch (score_kind(a)) {
+    case SC_PLAIN: return f(IntC<SC_PLAIN>{});
+    case SC_BIAS: return f(IntC<SC_BIAS>{});
+    case SC_CAP: return f(IntC<SC_CAP>{});
+    default: return f(IntC<SC_ANY>{});
+    }
 }
 
 // The weights are rounded to the activations' type before the second product.
@@ -361,16 +372,12 @@ inline int score_kind(const AttnArgs& a)
 // numerator (a row of one dominant key comes out as that key's value); the sum
 // of the unrounded ones is only kept where lse is asked for.
 
-// Score modification, in units of log 2: s is q . k on the codes.  Without a
-// cap c0 = k scale * softmax scale * log2 e; with one c0 = 2 log2 e * k scale *
-// softmax scale / cap and c1 = cap * log2 e: cap tanh(x) = cap (1 - 2 / (1 +
-// e^2x)), whose absolute error of 1e-7 cap is far under what 16-bit queries
-// carry, and which saturates at both ends.
-template <bool CAP>
-__device__ __forceinline__ float score(float s, float c0, float c1)
+// cap * tanh(x) - from, for s * c0 = 2 log2(e) x: cap (1 - 2 / (1 + e^2x)), whose
+// absolute error of 1e-7 cap is far under what 16-bit queries carry, and which
+// saturates at both ends.
+__device__ __forceinline__ float capped(float s, float c0, float cap, float from)
 {
-    if (!CAP) return s * c0;
-    return c1 * (1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * c0)));
+    return __builtin_fmaf(__builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(s * c0)), -2.0f * cap, cap - from);
 }
 
 constexpr float kLog2e = 1.4426950408889634f;

@@ -71,7 +71,7 @@ SHAPE_REFUSALS = [
     (dict(hkv=0), E_SHAPE), (dict(hq=7), E_SHAPE), (dict(max_q=-1), E_SHAPE), (dict(max_kv=-1), E_SHAPE),
     (dict(pages=-1), E_SHAPE), (dict(pages=0), E_SHAPE), (dict(stride=0), E_SHAPE), (dict(d=80), E_UNSUP),
     (dict(d=512), E_UNSUP), (dict(page=8), E_UNSUP), (dict(page=48), E_UNSUP), (dict(page=512), E_UNSUP),
-    (dict(hq=65536, hkv=1), E_UNSUP), (dict(tokens=2 ** 28), E_UNSUP), (dict(stride=2 ** 27), E_UNSUP),
+    (dict(hq=65536, hkv=1), E_UNSUP), (dict(tokens=2 ** 28), E_UNSUP), (dict(batch=2 ** 20 + 1), E_UNSUP), (dict(stride=2 ** 27), E_UNSUP),
 ]
 
 
