@@ -140,9 +140,9 @@ int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p)
 //   rows, 2 sequences x 4 heads, 131071 keys    8: 126   16: 71   32: 52   64: 59
 //   rows, 64 x 8, to 8192 keys                  1: 127    2: 133   4: 141
 //   rows, 1 x 2, 513 keys                       1: 7.6    3: 8.5 (the join's launch)
-//   tile, d = 64, 272 tiles of 12001 keys       1: 224    2: 174   3: 127   4: 150
-//   tile, d = 128, 8 tiles of 20000 keys        8: 71    16: 43   32: 34
-//   tile, d = 128, 2048 tiles (causal)          1: 303    2: 456 (the partial results' traffic)
+//   tile, d = 64, 272 tiles of 12001 keys       1: 234    2: 147   3: 110   4: 149
+//   tile, d = 128, 8 tiles of 20000 keys        8: 66    16: 41   32: 34   52: 39
+//   tile, d = 128, 2048 tiles (causal)          1: 278    2: 445 (the partial results' traffic)
 void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
     const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv);
@@ -159,8 +159,8 @@ void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
     const int64_t blocks = key_blocks(s, p);
     int64_t n = p->splits;
     if (n == 0) {
-        // one block a CU; of the tile form as many as a CU holds
-        const int64_t want = tile ? cus * (s->d <= 64 ? 3 : s->d <= 128 ? 2 : 1) : cus;
+        // one block a CU; of the tile form, if there are as many, what a CU holds
+        const int64_t want = tile && base >= cus ? cus * (s->d <= 64 ? 3 : s->d <= 128 ? 2 : 1) : cus;
         n = tile ? (want + base / 2) / base : base < want ? (want + base - 1) / base : 1;
         const int64_t most = tile ? (blocks + 23) / 24 : blocks < 64 ? 1 : (blocks + 15) / 16;
         n = n > most ? most : n;

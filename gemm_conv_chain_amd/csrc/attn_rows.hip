@@ -26,9 +26,9 @@ namespace fc {
 
 constexpr int AR_WAVES = 4;
 
-__device__ __forceinline__ u32x4 load_nt(const uint8_t* p)
+__device__ __forceinline__ u32x4 load_nt(global_u8* p)
 {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+    return __builtin_nontemporal_load((FC_GLOBAL const u32x4*)p);
 }
 
 template <class T, int D, int NT, int MODE>
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
         lds_poison((FC_LDS float*)lds, AR_WAVES * NT * (ND * 64 + 16) * 16, threadIdx.x, 64 * AR_WAVES);
         __syncthreads();
     }
-    const NoPage* no_page = &fc_no_page;
+    global_u8* no_page = global_at(&fc_no_page);
     asm("" : "+s"(no_page));   // the address is taken once, not by a load in every step
 
     {
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
         const int rows = nq * a.G;
         bool over;
         const int kv_len = seq_keys(a.kv_lens, s, b, &over), pos0 = kv_len - nq;
-        const uint8_t* const head = a.codes + side_base(0, h, 0, s);
+        global_u8* const head = global_at(a.codes) + side_base(0, h, 0, s);
         const size_t page_bytes = (size_t)s.hkv * 2 * s.page * D;
         const int side_bytes = s.page * D;
         for (int r0 = rb0 * R; r0 < rows; r0 += row_blocks * R) {
@@ -136,18 +136,18 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                     for (int t = 0; t < 4; ++t) {
                         const int it = __builtin_amdgcn_readlane(id, 16 * t);
                         const int kb = k0 + t < c1 ? k0 + t : c1 - 1;
-                        const uint8_t* src = it < 0 ? (const uint8_t*)no_page->codes[0]
-                                                    : head + it * page_bytes + (kb & ((1 << a.pg_shift) - 1)) * (16 * D);
+                        global_u8* src = it < 0 ? no_page : head + it * page_bytes + (kb & ((1 << a.pg_shift) - 1)) * (16 * D);
 #pragma unroll
                         for (int j = 0; j < NJ; ++j) kr[t][j] = load_nt(src + j * 1024 + lane * 16);
                     }
                 };
                 auto load_v = [&](int k0) {
-                    const uint8_t* src = id < 0 ? (const uint8_t*)no_page->codes[1]
-                                                : head + side_bytes + id * page_bytes +
-                                                      (block_of(k0) & ((1 << a.pg_shift) - 1)) * (16 * D);
-                    const float* scale = id < 0 ? no_page->scale : a.scales + ((size_t)id * s.hkv + h) * 2;
-                    sc = *reinterpret_cast<const floatx2*>(scale);
+                    global_u8* src = id < 0 ? no_page + 4096
+                                            : head + side_bytes + id * page_bytes +
+                                                  (block_of(k0) & ((1 << a.pg_shift) - 1)) * (16 * D);
+                    global_u8* scale = id < 0 ? no_page + offsetof(NoPage, scale)
+                                              : global_at(a.scales) + ((size_t)id * s.hkv + h) * 8;
+                    sc = *(FC_GLOBAL const floatx2*)scale;
 #pragma unroll
                     for (int d = 0; d < ND; ++d) vr[d] = load_nt(src + d * 256 + n * 16);
                 };

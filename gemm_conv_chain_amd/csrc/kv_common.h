@@ -11,6 +11,7 @@
 // scales [pages][kv heads][2]: a power of two for each page, head and side.
 #pragma once
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "fc_device.h"
@@ -347,6 +348,13 @@ __host__ __device__ constexpr NoPage make_no_page()
     return p;
 }
 static __device__ __align__(16) NoPage fc_no_page = make_no_page();
+
+// Global memory by its address space: a pointer chosen between the pool and
+// fc_no_page would otherwise be a generic one and its loads flat, and those are
+// waited for with the LDS reads.
+#define FC_GLOBAL __attribute__((address_space(1)))
+typedef FC_GLOBAL const uint8_t global_u8;
+__device__ __forceinline__ global_u8* global_at(const void* p) { return (global_u8*)p; }
 
 // Kinds of scores: scale * q . k alone; with a bias by distance (causal); capped;
 // everything else, a cap and a bias or a bias to both sides.
