@@ -10,8 +10,12 @@
 // rounded to nearest even: 4 bits of significand are the cache's choice.
 //
 // One block owns one (page, head), both sides, so that nothing is shared
-// between blocks: no atomics, and results do not depend on any order.  Waves
-// 0 .. WPS - 1 take K, the next WPS take V.
+// between blocks, and results do not depend on any order (the only atomics set
+// bits of a mask in LDS).  Waves 0 .. WPS - 1 take K, the next WPS take V.
+//
+// Bound by memory for prompts: six of them, 20 k tokens, 32 query heads, 8 kv
+// heads of 128: 499 MB in 112 us (4.4 TB/s; a copy reaches 4.8).  A step's token
+// is a chain of loads (lengths, page, values, scale): 8 us for 128 sequences.
 #include "fc_launch.h"
 #include "kv_common.h"
 
@@ -470,8 +474,8 @@ static long query_blocks(AppendArgs& a, int hpt, long mq, long threads)
 }
 
 // One launch: the blocks that append and those that turn queries are independent,
-// and the ones wait on chains of loads while the others stream (six prompts: 119
-// us; as two launches, 70 + 66).
+// and the ones wait on chains of loads while the others stream (six prompts, four
+// heads a thread: 119 us; as two launches, 70 + 66).
 template <class T, int WPS, int HPT>
 static hipError_t launch_append(AppendArgs a, hipStream_t st)
 {
@@ -486,14 +490,18 @@ static hipError_t launch_append(AppendArgs a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Waves a side by the page's values; a step's few tokens take a head a thread.
+// Waves a side by the page's values, and heads a thread that turns queries.
+// Measured for prompts of 5000 (us): pages of 16 x 64 values 88 with one wave a
+// side, 110 with two; 64 x 128 139 with two, 158 with four; 256 x 256 157 with
+// four, 190 with two.  Six prompts with pages of 32 x 128: 132, 112 and 118 with
+// one, two and four heads a thread; steps of few tokens want many threads.
 template <class T>
 static hipError_t pick_append(const AppendArgs& a, hipStream_t st)
 {
     if (a.s.max_q <= 16) return launch_append<T, 1, 1>(a, st);
     const int values = a.s.page * a.s.d;
-    if (values <= 2048) return launch_append<T, 1, 4>(a, st);
-    return values <= 8192 ? launch_append<T, 2, 4>(a, st) : launch_append<T, 4, 4>(a, st);
+    if (values <= 2048) return launch_append<T, 1, 2>(a, st);
+    return values <= 8192 ? launch_append<T, 2, 2>(a, st) : launch_append<T, 4, 2>(a, st);
 }
 
 hipError_t run_kv_append(int dtype, const void* k, const void* v, const void* q, void* q_out, const long* strides,
