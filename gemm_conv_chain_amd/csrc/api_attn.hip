@@ -106,8 +106,10 @@ fc::KvShape kv(const fc_kv_shape* s)
 fc_status check_params(const fc_kv_shape* s, const fc_attn_params* p)
 {
     if (!p) return fail(FC_E_NULL, "params is NULL");
-    if (!(p->scale > 0.0f) || p->scale > 1e30f) return fail(FC_E_ARG, "scale must be positive and finite");
-    if (!(p->softcap >= 0.0f) || p->softcap > 1e30f) return fail(FC_E_ARG, "softcap must be >= 0 and finite");
+    // (the kernels divide by either, and one by the other, in 32 bits)
+    if (!(p->scale >= 1e-18f && p->scale <= 1e18f)) return fail(FC_E_ARG, "scale must be positive, 1e-18 to 1e18");
+    if (p->softcap != 0.0f && !(p->softcap >= 1e-18f && p->softcap <= 1e18f))
+        return fail(FC_E_ARG, "softcap must be 0 or 1e-18 to 1e18");
     if (p->window < 0) return fail(FC_E_ARG, "window %d is negative", p->window);
     if (p->window > 0 && !p->causal) return fail(FC_E_UNSUPPORTED, "a window needs causal scores");
     if (p->variant < 0 || p->variant > 2) return fail(FC_E_ARG, "variant %d out of range", p->variant);

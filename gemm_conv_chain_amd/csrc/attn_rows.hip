@@ -21,7 +21,7 @@
 // joined through LDS and the blocks' by k_attn_join, both in a fixed order.
 // Measured: 64 sequences x 8 kv heads of 128, to 8192 keys, 756 MB in 127 us (5.9
 // TB/s); 2 x 4, 131071 keys, 269 MB in 53 us with the join; 24 x 16 heads of 256,
-// three tokens, a window of 4096, 786 MB in 137 us.
+// three tokens, a window of 4096, 786 MB in 135 us (5.8 TB/s).
 #include "fc_launch.h"
 #include "kv_common.h"
 

@@ -20,7 +20,7 @@
 // cycles of matrix instructions and about 800 of vector ones (32 exponentials, at
 // 8 cycles, are a third of these), two waves a SIMD fill each other's gaps, and
 // the clock sinks under the load.  Measured for two prompts of 4096 with 32 query
-// heads of 128: 275 to 295 us by box (930 to 1000 TFLOP/s; a library product of
+// heads of 128: 271 to 289 us by box (950 to 1015 TFLOP/s; a library product of
 // 8192^3 reaches 1170); without the exponentials, the widening and the maximum
 // the same loop still takes 227.
 #include "fc_launch.h"

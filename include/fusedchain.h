@@ -587,8 +587,8 @@ fc_status kv_append(const void *k, const void *v, const void *q, void *q_out, co
 typedef enum { FC_ATTN_AUTO = 0, FC_ATTN_ROWS = 1, FC_ATTN_TILE = 2 } fc_attn_variant;
 
 typedef struct {
-    float scale;        /* > 0: scores are scale * q . k */
-    float softcap;      /* > 0: softcap * tanh(score / softcap); 0: off */
+    float scale;        /* 1e-18 .. 1e18: scores are scale * q . k */
+    float softcap;      /* 1e-18 .. 1e18: softcap * tanh(score / softcap); 0: off */
     int32_t causal;     /* != 0: the query at slot s sees slots <= s */
     int32_t window;     /* > 0: it sees the last `window` of them (causal only); 0: all */
     int32_t variant;    /* fc_attn_variant */

@@ -117,6 +117,13 @@ def test_attn_refusals(L):
     assert b"workspace" in L.fc_last_error()
 
 
+def test_attn_refuses_scales_whose_quotient_leaves_32_bits(L):
+    for s in (1e-45, 9e-19, 1.1e18):
+        assert attn(L, scale=s) == E_ARG
+    for c in (1e-45, 9e-19, 1.1e18):
+        assert attn(L, cap=c) == E_ARG
+
+
 def test_plan():
     one = fc.attn_plan(1, 1, 8, 2, 64, 16, 40, 1, 513)
     assert one["variant"] == "rows"
