@@ -3,14 +3,15 @@
     python -m gemm_conv_chain_amd.rocprof_summary trace  DIR        # --kernel-trace --stats -f csv
     python -m gemm_conv_chain_amd.rocprof_summary pmc    DIR WORKLOAD [--json profiles/traffic.json]
     python -m gemm_conv_chain_amd.rocprof_summary mfma   DIR [WORKLOAD --json profiles/traffic.json]
-        (DIR from --pmc SQ_VALU_MFMA_BUSY_CYCLES SQ_INSTS_VALU_MFMA_MOPS_F16 GRBM_GUI_ACTIVE; run after pmc)
+        (DIR from --pmc SQ_VALU_MFMA_BUSY_CYCLES SQ_INSTS_VALU_MFMA_MOPS_F16 GRBM_GUI_ACTIVE, with
+         SQ_INSTS_VALU_MFMA_MOPS_BF16 for kernels on bf16; run after pmc)
     python -m gemm_conv_chain_amd.rocprof_summary lds    DIR
         (DIR from --pmc SQ_LDS_IDX_ACTIVE SQ_LDS_BANK_CONFLICT SQ_LDS_ADDR_CONFLICT SQ_INSTS_LDS
          SQ_ACTIVE_INST_LDS GRBM_GUI_ACTIVE)
 
 ``trace``: the kernel_stats.csv rows (calls, average/min/max duration).
 ``mfma``: matrix-core activity per dispatch of this library's kernels.  On
-MI355X one fp16 MFMA "MOP" is 512 FLOP (SQ_INSTS_VALU_MFMA_MOPS_F16 x 512 is
+MI355X one fp16 or bf16 MFMA "MOP" is 512 FLOP (SQ_INSTS_VALU_MFMA_MOPS_F16 x 512 is
 the executed FLOP count) and SQ_VALU_MFMA_BUSY_CYCLES is the sum over all
 SIMDs of their busy clocks (it equals executed FLOP / 1024, the fp16 rate of
 one SIMD per clock); GRBM_GUI_ACTIVE is summed over the 8 XCDs, so the
@@ -78,14 +79,17 @@ def mfma(d, workload=None, json_path=None):
     rows = _rows(os.path.join(d, "**", "*counter_collection.csv"))
     per = {}
     for r in rows:
-        if "fc::" in r["Kernel_Name"]:
+        if _ours(r["Kernel_Name"]):
             per.setdefault(r["Kernel_Name"], {}).setdefault(r["Counter_Name"], []).append(float(r["Counter_Value"]))
     print("| kernel | executed GFLOP (MOPS x 512) | MFMA busy (SIMD-clk) | GRBM_GUI_ACTIVE / 8 (clk) | MFMA busy fraction |")
     print("|---|---|---|---|---|")
     for k in sorted(per):
         v = {c: sum(x) / len(x) for c, x in per[k].items()}
-        mops, busy, act = (v.get(c, 0.0) for c in ("SQ_INSTS_VALU_MFMA_MOPS_F16", "SQ_VALU_MFMA_BUSY_CYCLES",
-                                                  "GRBM_GUI_ACTIVE"))
+        f16, bf16, busy, act = (v.get(c, 0.0) for c in ("SQ_INSTS_VALU_MFMA_MOPS_F16", "SQ_INSTS_VALU_MFMA_MOPS_BF16",
+                                                       "SQ_VALU_MFMA_BUSY_CYCLES", "GRBM_GUI_ACTIVE"))
+        if not busy:   # a kernel without matrix products
+            continue
+        mops = f16 + bf16
         frac = busy / (act / 8 * 1024) if act else 0.0
         print("| `%s` | %.3f | %.0f | %.0f | %.3f |" % (k[:90], mops * 512 / 1e9, busy, act / 8, frac))
         if json_path and workload:

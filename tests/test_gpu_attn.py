@@ -1,6 +1,7 @@
 """rope, kv_append and chain_attn on the GPU against plain implementations in 64
 bits (attn_ref), at the sizes, masks and layouts where they can go wrong."""
 import math
+import random
 
 import pytest
 
@@ -414,6 +415,29 @@ def test_empty_calls(fc):
     assert fc.chain_attn(z, codes, scales, *meta).shape == (0, 2, 64)
     assert fc.kv_append(z, z, codes, scales, *meta, q=z).shape == (0, 2, 64)
     assert fc.rope(z, meta[2][:0], fc.rope_turns(64)[0].cuda()).shape == (0, 2, 64)
+
+
+# ------------------------------------------------------------ drawn mixtures
+@pytest.mark.parametrize("seed", range(24))
+def test_attn_drawn(fc, seed):
+    """Sizes, heads, pages, masks, forms and splits drawn together."""
+    r = random.Random(seed)
+    dtype, d, page = DTYPES[seed % 2], (64, 128, 192, 256)[seed // 2 % 4], r.choice([16, 32, 64, 128, 256])
+    hkv, G = r.choice([1, 2, 3, 8]), r.choice([1, 2, 3, 4, 7])
+    lens = [r.choice([0, 1, 15, 16, 17, r.randrange(1, 900), r.randrange(1, 2500)]) for _ in range(r.randrange(1, 5))]
+    new = [min(n, r.choice([0, 1, 1, 2, 5, r.randrange(1, 150)])) for n in lens]
+    new[0] = max(new[0], 1)                  # at least one query, of which some see no key where lens[0] = 0
+    b = batch(seed + 900, dtype, lens, new, hkv * G, hkv, d, page)
+    kw = dict(causal=r.random() < 0.8, softcap=r.choice([0.0, 0.0, 20.0]))
+    if kw["causal"]:
+        kw["window"] = r.choice([0, 0, 1, 33, 500])
+    if r.random() < 0.3:
+        kw["slopes"] = torch.tensor([0.25 / (1 + h) for h in range(hkv * G)])
+    if r.random() < 0.5:
+        kw.update(variant=r.choice(["rows", "tile"]), splits=r.choice([0, 1, 2, 4]))
+    if r.random() < 0.5:
+        kw.update(max_q=max(new), max_kv=max(lens))
+    attend(fc, b, "drawn %d %s %s %s" % (seed, lens, new, (hkv * G, hkv, d, page)), dtype, **kw)
 
 
 # -------------------------------------------------- streams, graphs, debug build
