@@ -117,15 +117,55 @@ fc_status check_params(const fc_kv_shape* s, const fc_attn_params* p)
     return FC_OK;
 }
 
-// Blocks of 16 keys that the longest row can see.
-int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p)
+// Blocks of 16 keys that a block of `rows` rows can see.
+int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p, int64_t rows)
 {
     int64_t keys = s->max_kv > 0 ? s->max_kv : 1;
     const int64_t cap = (int64_t)s->page * s->table_stride;
     if (keys > cap && cap > 0) keys = cap;
-    // all rows of a launch see at most the window and what the queries span
-    if (p->window > 0 && (int64_t)p->window + s->max_q < keys) keys = (int64_t)p->window + s->max_q;
+    // the window and what the block's queries span
+    int64_t span = rows / (s->hq / s->hkv) + 1;
+    if (span > s->max_q) span = s->max_q;
+    if (p->window > 0 && p->window + span < keys) keys = p->window + span;
     return (keys + 15) / 16 + 1;
+}
+
+// Splits of the tile form: the least of
+//   max(1, (n * tiles / CUs + 1/2) / k) * (chunk + 5) * (d + 40) / 168       the products
+//   + 20 + 2 n * tokens * hq * d / 10^6, if n > 1                           partial results and join
+// where chunk is in blocks of 16 keys, tiles are those that `tokens` fill (fewer
+// than max_q allows if the batch is ragged), and a CU does the work of k = 1.5 (d =
+// 64: of three at a time), 2 (d = 128) or 1.5 tiles in the time of one.  More splits
+// have to gain 4 %.  The numbers are fits to 80 drawn calls (d = 64 to 256, 1 to 16
+// sequences, to 32768 keys, most of them ragged) timed with 1 to 16 splits: the choice
+// is 4 % from the best on average and 1.5 times it at worst; filling the machine once,
+// by max_q, was 14 % and 2.1 times.  (us, by splits, the choice marked:)
+//   d = 64, 138 tiles of 8000 keys, ragged      1: 122   2: 86   4: 70    6*: 59   8: 70
+//   d = 64, 584 tiles of 12001 keys             1: 511   2*: 420  4: 386   8: 434
+//   d = 128, 346 tiles of 4000 keys, ragged     1*: 110   2: 147   4: 141
+//   d = 64, 62 tiles of 16000 keys, ragged      1: 238   4: 75   8: 55   10: 68   (9 taken)
+//   d = 256, 8 tiles of 14400 keys              1: 890   4: 246   16: 87          (29 taken)
+int64_t tile_splits(const fc_kv_shape* s, int64_t per, int64_t base, int64_t blocks)
+{
+    const double rows = (double)s->tokens * (s->hq / s->hkv);
+    double tiles = s->hkv * (rows / per + 0.5 * s->batch);
+    if (tiles > base) tiles = (double)base;
+    if (tiles < s->hkv) tiles = s->hkv;
+    const double k = s->d == 128 ? 2.0 : 1.5, cus = fc::device_cu_count();
+    int64_t best = 1;
+    double least = 0.0;
+    for (int64_t n = 1; n <= 64 && (n - 1) * 8 < blocks; ++n) {
+        const int64_t chunk = ((blocks + n - 1) / n + 3) / 4 * 4;
+        if ((blocks + chunk - 1) / chunk < n) continue;   // fewer splits have this chunk
+        const double full = (n * tiles / cus + 0.5) / k;
+        double t = (full > 1.0 ? full : 1.0) * (chunk + 5) * (s->d + 40) / 168.0;
+        if (n > 1) t += 20.0 + 2e-6 * n * s->tokens * s->hq * s->d;
+        if (n == 1 || t < 0.96 * least) {
+            least = t;
+            best = n;
+        }
+    }
+    return best;
 }
 
 // Form and split of a call.  Few rows take the form whose waves split the keys,
@@ -137,14 +177,11 @@ int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p)
 //   8 x 4, 4000 keys     d = 64    64 rows 19 / 21     128 rows 26 / 24
 //                        d = 128   64 rows 24 / 29     96 rows 38 / 31
 //                        d = 256   64 rows 49 / 60     96 rows 77 / 63
-// Keys are split over blocks where rows and heads alone leave CUs without one
-// (us, by splits):
+// The rows form splits keys over blocks where rows and heads alone leave CUs
+// without one (us, by splits):
 //   rows, 2 sequences x 4 heads, 131071 keys    8: 126   16: 71   32: 52   64: 59
 //   rows, 64 x 8, to 8192 keys                  1: 127    2: 133   4: 141
 //   rows, 1 x 2, 513 keys                       1: 7.6    3: 8.5 (the join's launch)
-//   tile, d = 64, 272 tiles of 12001 keys       1: 234    2: 147   3: 110   4: 149
-//   tile, d = 128, 8 tiles of 20000 keys        8: 66    16: 41   32: 34   52: 39
-//   tile, d = 128, 2048 tiles (causal)          1: 278    2: 445 (the partial results' traffic)
 void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
     const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv);
@@ -158,13 +195,12 @@ void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
     const bool tile = v == FC_ATTN_TILE;
     const int64_t per = tile ? (s->d <= 128 ? 128 : 256) : (rows > 16 ? 32 : 16);   // rows a block
     const int64_t base = (int64_t)(s->batch > 0 ? s->batch : 1) * s->hkv * ((rows + per - 1) / per);
-    const int64_t blocks = key_blocks(s, p);
+    const int64_t blocks = key_blocks(s, p, per);
     int64_t n = p->splits;
-    if (n == 0) {
-        // one block a CU; of the tile form, if there are as many, what a CU holds
-        const int64_t want = tile && base >= cus ? cus * (s->d <= 64 ? 3 : s->d <= 128 ? 2 : 1) : cus;
-        n = tile ? (want + base / 2) / base : base < want ? (want + base - 1) / base : 1;
-        const int64_t most = tile ? (blocks + 23) / 24 : blocks < 64 ? 1 : (blocks + 15) / 16;
+    if (n == 0 && tile) n = tile_splits(s, per, base, blocks);
+    else if (n == 0) {
+        n = base < cus ? (cus + base - 1) / base : 1;   // one block a CU
+        const int64_t most = blocks < 64 ? 1 : (blocks + 15) / 16;
         n = n > most ? most : n;
         n = n > 256 ? 256 : n;
     }
