@@ -124,6 +124,18 @@ def test_attn_refuses_scales_whose_quotient_leaves_32_bits(L):
         assert attn(L, cap=c) == E_ARG
 
 
+def test_plan_of_tiles():
+    def tile(tokens, batch, max_q, max_kv, window=0, hkv=4, d=64):
+        p = fc.attn_plan(tokens, batch, 4 * hkv, hkv, d, 64, 512, max_q, max_kv, window=window, variant="tile")
+        assert p["splits"] * p["chunk"] >= min(max_kv, window + max_q if window else max_kv)
+        assert p["workspace"] == (tokens * 4 * hkv * p["splits"] * (d + 4) * 4 if p["splits"] > 1 else 0)
+        return p["splits"]
+    assert tile(64, 1, 64, 20000) > 16                        # eight tiles: the keys fill the machine
+    assert tile(64, 1, 64, 20000, window=100) == 1            # but a windowed tile sees few of them
+    assert tile(4096, 1, 4096, 4096, hkv=32) == 1             # 4096 tiles fill it
+    assert tile(1100, 4, 800, 9000) >= tile(3200, 4, 800, 9000)   # a ragged batch has fewer tiles than max_q allows
+
+
 def test_plan():
     one = fc.attn_plan(1, 1, 8, 2, 64, 16, 40, 1, 513)
     assert one["variant"] == "rows"
