@@ -94,7 +94,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                 const int r = r0 + 16 * c + n, rr = r < rows ? r : rows - 1;
                 const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G);
                 pos[c] = pos0 + t;
-                slope[c] = (MODE == SC_BIAS || MODE == SC_ANY) && a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
+                slope[c] = may_bias(MODE) && a.slopes ? a.slopes[hq] * kLog2e : 0.0f;
                 const T* q = (const T*)a.q + (tok0 + t) * a.q_ts + (long)hq * a.q_hs;
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
             const int all_hi = a.causal ? (pos0 + t_first + 1 < kv_len ? pos0 + t_first + 1 : kv_len) : kv_len;
 
             // scores in units of log 2 are q . k on the codes, times the page's scale, times this
-            const bool cap = MODE == SC_CAP || (MODE == SC_ANY && a.cap > 0.0f);
+            const bool cap = MODE == SC_CAP || MODE == SC_FAR || (MODE == SC_ANY && a.cap > 0.0f);
             const float factor = cap ? 2.0f * kLog2e * a.scale / a.cap : a.scale * kLog2e;
             floatx4 o[NT][ND];
             float m[NT], l[NT], le[NT];   // maximum; sums of rounded and (for lse) of exact weights
@@ -198,9 +198,11 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const float y = st[c][i >> 2][i & 3];
-                            x[i] = cap ? capped(y, ft[i >> 2], a.cap * kLog2e, 0.0f) : y * ft[i >> 2];
+                            x[i] = MODE == SC_FAR ? capped_far(y, ft[i >> 2], a.cap * kLog2e, 0.0f)
+                                   : cap          ? capped(y, ft[i >> 2], a.cap * kLog2e, 0.0f)
+                                                  : y * ft[i >> 2];
                         }
-                        if (MODE == SC_BIAS || MODE == SC_ANY) {
+                        if (may_bias(MODE)) {
                             const float gap = (float)(pos[c] - key0);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) x[i] -= slope[c] * fabsf(gap - (float)((i >> 2) * 16 + (i & 3)));

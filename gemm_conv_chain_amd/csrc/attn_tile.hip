@@ -99,7 +99,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
             // this lane's row
             const int r = w0 + n, rr = r < rows ? r : rows - 1;
             const int t = a.by_g.div(rr), hq = h * a.G + (rr - t * a.G), pos = pos0 + t;
-            const float slope = (MODE == SC_BIAS || MODE == SC_ANY) && a.slopes ? a.slopes[hq] * (MODE == SC_BIAS ? 1.0f / a.scale : kLog2e) : 0.0f;
+            const float slope = may_bias(MODE) && a.slopes ? a.slopes[hq] * (MODE == SC_BIAS ? 1.0f / a.scale : kLog2e) : 0.0f;
             v8 qf[NK];
             {
                 const T* q = (const T*)a.q + (tok0 + t) * a.q_ts + (long)hq * a.q_hs;
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                 for (int j = 0; j < NK; ++j) qf[j] = *reinterpret_cast<const v8*>(q + 16 * (2 * (j >> 1) + hf) + 8 * (j & 1));
             }
             // x * unit: the exponent of 2; of the capped and general kinds x is that already
-            const float unit = MODE == SC_CAP || MODE == SC_ANY ? 1.0f : a.scale * kLog2e, lag = 8.0f / unit;
+            const float unit = MODE != SC_PLAIN && MODE != SC_BIAS ? 1.0f : a.scale * kLog2e, lag = 8.0f / unit;
             const float cap0 = 2.0f * kLog2e * a.scale / (a.cap > 0.0f ? a.cap : 1.0f);
             floatx16 o[ND];
 #pragma unroll
@@ -227,15 +227,16 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                     }
                     load(k0 + 2 * KB, id);
                     id = load_id(k0 + 3 * KB);
-                    if (MODE == SC_CAP || MODE == SC_ANY) {
+                    if (MODE != SC_PLAIN && MODE != SC_BIAS) {
 #pragma unroll
                         for (int u = 0; u < U; ++u) {
                             const float gap = (float)(pos - key0 - 32 * u);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
-                                const float bias = MODE == SC_ANY ? __builtin_fmaf(slope, fabsf(gap - (float)i), mb) : mb;
-                                x[u][i] = MODE == SC_CAP || a.cap > 0.0f ? capped(x[u][i], cap0, a.cap * kLog2e, bias)
-                                                                         : x[u][i] * (a.scale * kLog2e) - bias;
+                                const float bias = may_bias(MODE) ? __builtin_fmaf(slope, fabsf(gap - (float)i), mb) : mb;
+                                x[u][i] = MODE == SC_FAR                   ? capped_far(x[u][i], cap0, a.cap * kLog2e, bias)
+                                          : MODE == SC_CAP || a.cap > 0.0f ? capped(x[u][i], cap0, a.cap * kLog2e, bias)
+                                                                           : x[u][i] * (a.scale * kLog2e) - bias;
                             }
                         }
                     }
