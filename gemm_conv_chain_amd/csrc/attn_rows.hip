@@ -41,6 +41,9 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
     constexpr int R = 16 * NT;       // rows a block
     constexpr int NJ = D / 64;       // 16-byte loads of K a lane and tile
     constexpr int ND = D / 16;       // tiles of V^T
+    constexpr int UP = Tr<T>::up;    // weights, at most 1, times 2^UP
+    // (the largest score's argument is exactly 0, whatever its size, so that 2^UP is not passed)
+    auto weight = [](float x) { return __builtin_amdgcn_exp2f(UP ? x + (float)UP : x); };
     const KvShape& s = a.s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -235,7 +238,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                         unsigned w[4][2];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            const float p0 = __builtin_amdgcn_exp2f(x[i] - ms), p1 = __builtin_amdgcn_exp2f(x[i + 1] - ms);
+                            const float p0 = weight(x[i] - ms), p1 = weight(x[i + 1] - ms);
                             w[i >> 2][(i >> 1) & 1] = Tr<T>::pk(p0, p1);
                             sum = Tr<T>::add2(w[i >> 2][(i >> 1) & 1], sum);
                             exact += p0 + p1;
@@ -295,7 +298,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
 #pragma unroll
             for (int c = 0; c < NT; ++c) {
                 l[c] = sum_x32(sum_x16(l[c]));
-                le[c] = sum_x32(sum_x16(le[c]));
+                le[c] = sum_x32(sum_x16(le[c])) * (1.0f / (1 << UP));
                 if (g == 0) lds_ml[(wave * NT + c) * 16 + n] = floatx4{m[c], l[c], le[c], 0.0f};
             }
             __syncthreads();

@@ -50,6 +50,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
     constexpr int PW = 2 * KB * NP / NW;     // pieces of 1 KiB of codes a wave and stage
     static_assert(2 * KB * NP % NW == 0 && 2 * NP % PW == 0, "a wave's pieces are of one block");
     constexpr int AH = D == 64 ? 4 : 2;   // operands read ahead (d = 64 with a bias: 126 us, with two 152)
+    constexpr int LAG = 8, UP = Tr<T>::up > LAG ? Tr<T>::up - LAG : 0;   // weights are at most 2^(LAG + UP)
     const KvShape& s = a.s;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
@@ -107,12 +108,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                 for (int j = 0; j < NK; ++j) qf[j] = *reinterpret_cast<const v8*>(q + 16 * (2 * (j >> 1) + hf) + 8 * (j & 1));
             }
             // x * unit: the exponent of 2; of the capped and general kinds x is that already
-            const float unit = MODE != SC_PLAIN && MODE != SC_BIAS ? 1.0f : a.scale * kLog2e, lag = 8.0f / unit;
+            const float unit = MODE != SC_PLAIN && MODE != SC_BIAS ? 1.0f : a.scale * kLog2e, top_x = (LAG + UP) / unit;
             const float cap0 = 2.0f * kLog2e * a.scale / (a.cap > 0.0f ? a.cap : 1.0f);
             floatx16 o[ND];
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[d] = zero16();
-            float m = kNegInf, mb = 0.0f;   // the maximum that weights refer to; with 0 for -inf
+            float m = kNegInf, mb = 0.0f;   // what weights refer to, a maximum less UP; with 0 for -inf
             float l = 0.0f, le = 0.0f;      // sums of rounded and (for lse) of exact weights
 
             for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
@@ -256,11 +257,12 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                     float mx = x[0][0];
 #pragma unroll
                     for (int i = 1; i < 16 * U; ++i) mx = fmaxf(mx, x[i >> 4][i & 15]);
-                    mx = max_x32(mx) + mb;
-                    // Weights refer to a maximum that may lag by a factor of 2^8, so that most stages do
-                    // not touch the accumulators: a weight is at most 256, as exact as one of at most 1.
-                    if (__any(mx > m + lag)) {
-                        const float mn = fmaxf(m, mx), to = mn == kNegInf ? 0.0f : mn;
+                    mx = max_x32(mx);
+                    // Weights refer to a maximum that may lag by a factor of 2^LAG, so that most stages do
+                    // not touch the accumulators: a weight is as exact as if it were at most 1.
+                    if (__any(mx > (m == kNegInf ? kNegInf : top_x))) {
+                        const float below = UP ? top_x * (UP / (float)(LAG + UP)) : 0.0f;
+                        const float mn = fmaxf(m, mx + mb - below), to = mn == kNegInf ? 0.0f : mn;
                         const float by = to - mb;
                         const float alpha = __builtin_amdgcn_exp2f((m - to) * unit);
                         m = mn;
@@ -271,6 +273,11 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                         for (int d = 0; d < ND; ++d) o[d] *= alpha;
 #pragma unroll
                         for (int i = 0; i < 16 * U; ++i) x[i >> 4][i & 15] -= by;
+                        // where a step of 32-bit scores is not small, the reference is off by as much
+                        if (UP && __any(fabsf(to) * unit > 0x1p20f)) {
+#pragma unroll
+                            for (int i = 0; i < 16 * U; ++i) x[i >> 4][i & 15] = x[i >> 4][i & 15] > top_x ? top_x : x[i >> 4][i & 15];
+                        }
                     }
                     if (a.lse) {   // (their weights once more, rather than a sum that other calls pay for)
                         float exact = 0.0f;

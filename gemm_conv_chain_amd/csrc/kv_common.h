@@ -44,6 +44,7 @@ template <class T> struct Tr;
 template <> struct Tr<half_t> {
     typedef half8 v8;
     static constexpr int elo = -15, ehi = 7;    // scale exponents: code * scale is exactly an fp16 value
+    static constexpr int up = 15;               // 2^up is a value of the type: see the weights below
     __device__ static __forceinline__ unsigned from_fp8(unsigned w, float s, bool hi)
     {
         return hi ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, s, true))
@@ -75,6 +76,7 @@ template <> struct Tr<half_t> {
 template <> struct Tr<bf16_t> {
     typedef bf8 v8;
     static constexpr int elo = -100, ehi = 119;
+    static constexpr int up = 0;                // (the type has the range of 32 bits)
     __device__ static __forceinline__ unsigned from_fp8(unsigned w, float s, bool hi)
     {
         return hi ? __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, s, true))
@@ -382,8 +384,12 @@ template <class F> inline hipError_t by_kind(const AttnArgs& a, F&& f)
 
 // The weights are rounded to the activations' type before the second product.
 // The sum that divides the result is of the rounded ones, so that it matches its
-// numerator (a row of one dominant key comes out as that key's value); the sum
-// of the unrounded ones is only kept where lse is asked for.
+// numerator (a row of one dominant key comes out as that key's value); lse takes
+// the sum of the unrounded ones.  fp16 weights are lifted by a power of two, which
+// the division takes out again, to the top of the type's range: with the largest at
+// 1, those under 2^-14 would lose bits and those under 2^-25 vanish, and a long flat
+// tail under one dominant key with them (131071 keys 17.4 below it are 0.36 % of
+// the result); lifted, a weight is rounded by 2^-32 of the largest at most.
 
 // cap * tanh(t) - from, for s * c0 = 2 log2(e) t: cap (1 - 2 / (1 + e^2t)), which
 // saturates at both ends.  Its error is absolute, up to 3e-7 cap however small the

@@ -1,5 +1,6 @@
 """chain_attn where its arithmetic is stretched, on the GPU against 64 bits: caps
-far above the scores."""
+far above the scores, long flat tails under a dominant key, scores near the end of
+32-bit resolution."""
 import math
 
 import pytest
@@ -28,12 +29,14 @@ def cap_error(x, cap):
 
 def attention(b, scale=None, causal=True, softcap=0.0, window=0, slopes=None):
     """(out, tolerance before the output's rounding, lse, lse tolerance), for
-    sequences of at least one key."""
+    sequences of at least one key.  Weights are rounded to the type relative to
+    their size, except that fp16's below 2^-14 lose a fixed 2^-25: the largest
+    weight of a row is 2^7 or more, so that is 2^-32 of it for each key."""
     q, codes, scales, table, cu_q, kv_lens = (b[k] for k in ("q", "codes", "scales", "table", "cu_q", "kv_lens"))
     T, hq, d = q.shape
     G = hq // codes.shape[1]
     u = R.half_step(q.dtype)
-    lost = R.TINY[q.dtype]
+    lost = 2.0 ** -32 if q.dtype == F16 else 0.0
     scale = d ** -0.5 if scale is None else scale
     out, tol = torch.zeros((2, T, hq, d), dtype=torch.float64)
     lse, ltol = torch.full((T, hq), -math.inf, dtype=torch.float64), torch.zeros((T, hq), dtype=torch.float64)
@@ -124,3 +127,62 @@ def test_caps_with_most_keys_far_below(fc, variant, splits):  # noqa: F811
     b["codes"][:, :, 0] = R.pack_k(K.reshape(K.shape[0], 2, 1, 16, 64))
     b["scales"][:, :, 0] = 2.0 ** -4
     attend(fc, b, "most keys far below", variant, splits, scale=0.5, softcap=300.0)
+
+
+# ------------------------------------------------------------------- flat tails
+def tail_batch(dtype, n, d=64, page=128):
+    """One sequence whose first key is 16, 17, 17.4 and 18 above the others for the
+    four heads, with values near 1 behind the others and 0 behind it."""
+    g = gen(79)
+    pages = -(-n // page)
+    K = torch.randn((pages, 1, page, d), generator=g) * 0.375
+    V = 1.0 + torch.randn((pages, 1, page, d), generator=g) / 4
+    K[:, :, :, 0] = 0.0
+    K[0, 0, 0] = 0.0
+    K[0, 0, 0, 0] = 16.0
+    V[0, 0, 0] = 0.0
+    codes = torch.empty((pages, 1, 2, page // 16, 16 * d), dtype=torch.uint8)
+    codes[:, :, 0] = R.pack_k(R.encode(K).reshape(pages, 1, page // 16, 16, d))
+    codes[:, :, 1] = R.pack_v(R.encode(V).reshape(pages, 1, page // 16, 16, d))
+    q = torch.randn((1, 4, d), generator=g) / 4
+    q[0, :, 0] = torch.tensor([8.0, 8.5, 8.7, 9.0])
+    return dict(q=q.to(dtype), codes=codes, scales=torch.ones((pages, 1, 2)),
+                table=torch.arange(pages, dtype=torch.int32)[None], cu_q=i32([0, 1]), kv_lens=i32([n]))
+
+
+@pytest.mark.parametrize("variant,splits", FORMS + [("rows", 40), ("tile", 40)])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [40000, 131071])
+def test_flat_tail_under_a_dominant_key(fc, variant, splits, dtype, n):  # noqa: F811
+    """The tail's small weights, of which there are many, are not lost."""
+    attend(fc, tail_batch(dtype, n), "tail of %d %s" % (n, dtype), variant, splits)
+
+
+@pytest.mark.parametrize("variant,splits", FORMS)
+@pytest.mark.parametrize("every", [8, 64])
+def test_scores_whose_steps_are_coarse(fc, variant, splits, every):  # noqa: F811
+    """Scores of 2^27 and more, where neighbours in 32 bits are 16 apart (in units
+    of log 2): weights stay inside fp16's range, results among the values."""
+    n, d, page = 200, 64, 16
+    pages = 13
+    K, V = torch.zeros((pages, 1, page, d)), torch.randn((pages, 1, page, d), generator=gen(83))
+    K[:, :, :, 0] = 128.0
+    for p in range(pages):
+        for t in range(page):
+            K[p, 0, t, 1] = (p * page + t) // every          # a step of 16 above the keys before
+    codes = torch.empty((pages, 1, 2, 1, 16 * d), dtype=torch.uint8)
+    codes[:, :, 0] = R.pack_k(R.encode(K).reshape(pages, 1, 1, 16, d))
+    codes[:, :, 1] = R.pack_v(R.encode(V).reshape(pages, 1, 1, 16, d))
+    scales = torch.ones((pages, 1, 2))
+    scales[:, :, 0] = 2.0 ** 7
+    q = torch.zeros((1, 2, d))
+    q[:, :, 0] = 2.0 ** 13
+    q[:, :, 1] = 2.0 ** -3
+    b = dict(q=q.half(), codes=codes, scales=scales, table=torch.arange(pages, dtype=torch.int32)[None],
+             cu_q=i32([0, 1]), kv_lens=i32([n]))
+    vals = R.values(R.encode(V)).abs().max()
+    for scale in (0.69314, math.log(2.0), 0.6932, 4.0 * math.log(2.0)):
+        print("case coarse", variant, splits, scale, flush=True)
+        out = fc.chain_attn(**on_gpu(b), scale=scale, variant=variant, splits=splits).cpu().double()
+        assert torch.isfinite(out).all(), scale
+        assert out.abs().max() <= vals * (1 + 2.0 ** -10), scale
