@@ -79,7 +79,7 @@ fc_status check_shape(const fc_kv_shape* s)
     // grid sizes, rows of a sequence and key positions are 32-bit
     if (s->batch > (1 << 20)) return fail(FC_E_UNSUPPORTED, "batch=%d exceeds 2^20", s->batch);
     if (s->hq > 65535) return fail(FC_E_UNSUPPORTED, "hq=%d exceeds 65535", s->hq);
-    if (s->tokens * s->hq > 0x3fffffffL) return fail(FC_E_UNSUPPORTED, "tokens*hq exceeds 2^30 - 1");
+    if (s->tokens > 0x3fffffffL / s->hq) return fail(FC_E_UNSUPPORTED, "tokens*hq exceeds 2^30 - 1");
     if ((int64_t)s->page * s->table_stride > 0x7fff0000L)
         return fail(FC_E_UNSUPPORTED, "page*table_stride exceeds the 32-bit positions");
     return FC_OK;

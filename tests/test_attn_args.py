@@ -1,0 +1,23 @@
+"""Host-only: arguments at the ends of their ranges, of the C entry points and of
+the binding."""
+import pytest
+
+import gemm_conv_chain_amd as fc
+
+torch = pytest.importorskip("torch")
+import test_attn_abi as A  # noqa: E402
+
+pytestmark = pytest.mark.cpu
+
+
+@pytest.fixture(scope="module")
+def L():
+    return fc.lib()
+
+
+@pytest.mark.parametrize("tokens,hq,hkv", [(2 ** 62, 4, 2), (2 ** 61 + 1, 8, 2), (2 ** 63 - 1, 2, 2), (2 ** 30, 1, 1)])
+def test_tokens_whose_rows_pass_64_bits(L, tokens, hq, hkv):
+    kw = dict(tokens=tokens, hq=hq, hkv=hkv)
+    assert A.attn(L, **kw) == A.E_UNSUP and A.append(L, **kw) == A.E_UNSUP
+    plan = fc.AttnPlan()
+    assert L.chain_attn_plan(A.shape(**kw), fc.AttnParams(0.125, 0, 1, 0, 0, 0), plan) == A.E_UNSUP
