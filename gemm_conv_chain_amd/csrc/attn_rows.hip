@@ -106,7 +106,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                         qf[c][2 * j + e] = *reinterpret_cast<const v8*>(q + 16 * (4 * j + g) + 8 * e);
             }
             // keys that every row of the tile sees need no mask
-            const int all_lo = a.window > 0 ? pos0 + t_last - a.window + 1 : 0;
+            const int all_lo = first_seen(a, pos0 + t_last);
             const int all_hi = a.causal ? (pos0 + t_first + 1 < kv_len ? pos0 + t_first + 1 : kv_len) : kv_len;
 
             // scores in units of log 2 are q . k on the codes, times the page's scale, times this
@@ -213,7 +213,7 @@ __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_
                         if (masked) {
                             int top = a.causal && pos[c] + 1 < kv_len ? pos[c] + 1 : kv_len;
                             top = (top < c1 * 16 ? top : c1 * 16) - key0;
-                            const int low = (a.window > 0 ? pos[c] - a.window + 1 : 0) - key0;
+                            const int low = first_seen(a, pos[c]) - key0;
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const int k = (i >> 2) * 16 + (i & 3);

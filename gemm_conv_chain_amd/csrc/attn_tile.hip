@@ -95,7 +95,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
             const int t_first = a.by_g.div(live ? w0 : r0), t_last = a.by_g.div(live ? w1 - 1 : r0);
             int wg_lo, wg_hi;
             key_range(a, kv_len, pos0, t_first, t_last, &wg_lo, &wg_hi);
-            const int all_lo = a.window > 0 ? pos0 + t_last - a.window + 1 : 0;
+            const int all_lo = first_seen(a, pos0 + t_last);
             const int all_hi = a.causal ? (pos0 + t_first + 1 < kv_len ? pos0 + t_first + 1 : kv_len) : kv_len;
             // this lane's row
             const int r = w0 + n, rr = r < rows ? r : rows - 1;
@@ -244,7 +244,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                     if (k0 * 16 < all_lo || (k0 + KB) * 16 > all_hi || k0 + KB > c1) {
                         int top = a.causal && pos + 1 < kv_len ? pos + 1 : kv_len;
                         top = (top < c1 * 16 ? top : c1 * 16) - key0;
-                        const int low = (a.window > 0 ? pos - a.window + 1 : 0) - key0;
+                        const int low = first_seen(a, pos) - key0;
 #pragma unroll
                         for (int u = 0; u < U; ++u)
 #pragma unroll

@@ -324,13 +324,19 @@ struct AttnArgs {
     FastDiv by_g;
 };
 
+// The first key that a query at `pos` sees (no difference of the two leaves 32 bits,
+// whatever the window and for positions before 0 too).
+__device__ __forceinline__ int first_seen(const AttnArgs& a, int pos)
+{
+    return a.window > 0 && pos >= a.window ? pos - a.window + 1 : 0;
+}
+
 // The keys that rows r0 .. r1 - 1 (of q_len * G) may see, as blocks of 16
 // [*g0, *g1), and the first query's position.
 __device__ __forceinline__ void key_range(const AttnArgs& a, int kv_len, int pos0, int t0, int t1, int* g0, int* g1)
 {
-    int lo = a.window > 0 ? pos0 + t0 - a.window + 1 : 0;
+    const int lo = first_seen(a, pos0 + t0);
     int hi = a.causal ? pos0 + t1 + 1 : kv_len;   // t1: the last query
-    lo = lo < 0 ? 0 : lo;
     hi = hi > kv_len ? kv_len : hi;
     *g0 = lo >> 4;
     *g1 = hi > lo ? (hi + 15) >> 4 : *g0;

@@ -1,6 +1,6 @@
 """chain_attn where its arithmetic is stretched, on the GPU against 64 bits: caps
 far above the scores, long flat tails under a dominant key, scores near the end of
-32-bit resolution."""
+32-bit resolution, windows at the end of the 32-bit integers."""
 import math
 
 import pytest
@@ -186,3 +186,16 @@ def test_scores_whose_steps_are_coarse(fc, variant, splits, every):  # noqa: F81
         out = fc.chain_attn(**on_gpu(b), scale=scale, variant=variant, splits=splits).cpu().double()
         assert torch.isfinite(out).all(), scale
         assert out.abs().max() <= vals * (1 + 2.0 ** -10), scale
+
+
+# ---------------------------------------------------------------------- windows
+@pytest.mark.parametrize("variant,splits", FORMS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+def test_windows_of_any_size(fc, variant, splits, window):  # noqa: F811
+    """A window that no sequence fills is none, for queries before slot 0 too."""
+    b = batch(89, BF16, [40, 300], [64, 3], 4, 2, 128, 16)
+    want = fc.chain_attn(**on_gpu(b), variant=variant, splits=splits)
+    print("case window", variant, splits, window, flush=True)
+    assert torch.equal(fc.chain_attn(**on_gpu(b), variant=variant, splits=splits, window=window), want)
+    ref, tol, _, _ = R.attention(**b)
+    R.assert_within(want, ref, R.rounded_tol(ref, tol, BF16), "window %d" % window)
