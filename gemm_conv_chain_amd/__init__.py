@@ -1014,7 +1014,8 @@ def kv_check(table, cu_q, kv_lens, pages, page, tokens=None, writes=False):
 
 def _attn_params(d, scale, causal, softcap, window, variant, splits):
     v = ATTN_VARIANT[variant] if isinstance(variant, str) else int(variant)
-    return AttnParams(d ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, int(window), v, int(splits))
+    window = max(-1, min(int(window), 0x7fffffff))   # (ctypes would keep the low 32 bits)
+    return AttnParams(d ** -0.5 if scale is None else scale, softcap, 1 if causal else 0, window, v, int(splits))
 
 
 _ATTN_VARIANT_NAME = {v: k for k, v in ATTN_VARIANT.items()}

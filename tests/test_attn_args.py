@@ -21,3 +21,15 @@ def test_tokens_whose_rows_pass_64_bits(L, tokens, hq, hkv):
     assert A.attn(L, **kw) == A.E_UNSUP and A.append(L, **kw) == A.E_UNSUP
     plan = fc.AttnPlan()
     assert L.chain_attn_plan(A.shape(**kw), fc.AttnParams(0.125, 0, 1, 0, 0, 0), plan) == A.E_UNSUP
+
+
+def test_windows_past_32_bits():
+    """A window that does not fit the C type is no window, not a smaller one."""
+    kw = dict(tokens=1, batch=1, hq=8, hkv=1, d=128, page=64, table_stride=2048, max_q=1, max_kv=131072)
+    none = fc.attn_plan(**kw)
+    assert fc.attn_plan(window=512, **kw) != none
+    for w in (2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 512, 2 ** 63 - 1, 10 ** 30):
+        assert fc.attn_plan(window=w, **kw) == none
+    for w in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 512, -2 ** 70):
+        with pytest.raises(fc.FusedChainError):
+            fc.attn_plan(window=w, **kw)

@@ -190,7 +190,7 @@ def test_scores_whose_steps_are_coarse(fc, variant, splits, every):  # noqa: F81
 
 # ---------------------------------------------------------------------- windows
 @pytest.mark.parametrize("variant,splits", FORMS)
-@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5, 2 ** 31, 2 ** 32 + 3, 2 ** 63 - 1])
 def test_windows_of_any_size(fc, variant, splits, window):  # noqa: F811
     """A window that no sequence fills is none, for queries before slot 0 too."""
     b = batch(89, BF16, [40, 300], [64, 3], 4, 2, 128, 16)
