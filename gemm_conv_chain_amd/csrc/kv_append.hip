@@ -37,11 +37,9 @@ __device__ __forceinline__ unsigned max_abs16(unsigned m, unsigned w)
 }
 __device__ __forceinline__ unsigned max_half(unsigned m) { return (m & 0xffffu) > (m >> 16) ? m & 0xffffu : m >> 16; }
 
-// Bits from which on a value is infinite or NaN; and, for keys, from which on
-// their rotation might overflow 32 bits.
+// Bits from which on a value is infinite or NaN.
 template <class T> struct Odd {
     static constexpr unsigned value = Tr<T>::elo == Tr<half_t>::elo ? 0x7c00u : 0x7f80u;
-    static constexpr unsigned key = Tr<T>::elo == Tr<half_t>::elo ? 0x7c00u : 0x7e00u;
 };
 template <class T> __device__ __forceinline__ float value16(unsigned bits)
 {
@@ -230,7 +228,9 @@ __device__ __forceinline__ void append_page(const AppendArgs& a, int b, int h, i
                         floatx4{y[j], y[j + 1], y[j + 2], y[j + 3]};
             }
         }
-        rare = max_half(top) >= Odd<T>::key;
+        // (finite keys may leave 32 bits as they turn: one of the pair is infinite then, the other may be
+        // NaN, which amax passes over)
+        rare = max_half(top) >= Odd<T>::value || !(amax < __builtin_inff());
     } else {
         unsigned all = 0;
         for (int i = tid; i < nwhole; i += NT) {
