@@ -55,6 +55,7 @@ fc_status check_rope(const fc_rope* r, int d)
         return fail(FC_E_SHAPE, "rot=%d must be a multiple of 16, at most d=%d", r->rot, d);
     if (r->rot > 0 && !r->turns) return fail(FC_E_NULL, "rope turns are required");
     if (!aligned(r->turns, 8)) return fail(FC_E_ALIGN, "rope turns must be 8-byte aligned");
+    if (!(r->mscale - r->mscale == 0.0f)) return fail(FC_E_ARG, "mscale must be a finite number");
     return FC_OK;
 }
 

@@ -542,7 +542,7 @@ typedef struct {
  * round(f / (2 pi) * 2^64)), so that an angle is exact at every 32-bit
  * position.  The first rot (a multiple of 16, <= d) elements of a head turn:
  * element i with i + rot/2, or 2i with 2i + 1 if interleaved.  mscale
- * multiplies both results. */
+ * multiplies both results; it has to be finite. */
 typedef struct {
     const int64_t *turns;
     int32_t rot, interleaved;

@@ -1,5 +1,7 @@
 """Host-only: arguments at the ends of their ranges, of the C entry points and of
 the binding."""
+import math
+
 import pytest
 
 import gemm_conv_chain_amd as fc
@@ -33,3 +35,12 @@ def test_windows_past_32_bits():
     for w in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 512, -2 ** 70):
         with pytest.raises(fc.FusedChainError):
             fc.attn_plan(window=w, **kw)
+
+
+@pytest.mark.parametrize("mscale", [math.nan, math.inf, -math.inf])
+def test_factors_that_are_no_numbers(L, mscale):
+    r = fc.RopeTable(0x10000, 64, 0, mscale)
+    assert L.rope_apply(A.P, A.P, A.strides(512, 64, 512, 64), A.P, r, 0, 0, 4, 8, 64, None) == A.E_ARG
+    st = A.strides(*[8] * 6)
+    assert L.kv_append(A.P, A.P, None, None, st, A.P, A.P, A.P, A.P, A.P, None, r, A.shape(), None) == A.E_ARG
+    assert b"mscale" in L.fc_last_error()
