@@ -840,7 +840,7 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=4.0, device=None):
+def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1.0, high=None, device=None):
     """(turns, mscale) of a rotary table: turns int64 [rot / 2], pair i's turns a
     position as 64-bit fractions (2^64 = one turn).  Without scaling pair i's
     frequency is f_i = base^(-2 i / rot) radians a position.  scaling, for
@@ -849,13 +849,17 @@ def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1
     * "linear"       f_i / factor;
     * "base"         base raised to base * factor^(rot / (rot - 2)), which leaves the
                      first pair as it is and stretches the last by factor;
-    * "wavelength"   pairs that turn at least ``high`` times within ``original``
-                     positions stay, those that turn at most ``low`` times are
-                     divided by factor, those between blend linearly in their
-                     number of turns;
+    * "wavelength"   pairs that turn at least ``high`` (4 by default) times within
+                     ``original`` positions stay, those that turn at most ``low``
+                     times are divided by factor, those between blend linearly in
+                     their number of turns;
     * "ramp"         the same with the blend linear in the pair's index (between
-                     the indices where ``high``, 32 by custom, and ``low`` turns
+                     the indices where ``high``, 32 by default, and ``low`` turns
                      are reached), and mscale = 0.1 ln(factor) + 1.
+
+    The last two are the by-parts interpolation of Peng et al., "YaRN: efficient
+    context window extension of large language models" (2023), in the forms that
+    models are trained with.
     """
     torch = _torch()
     if rot <= 0 or rot % 16:
@@ -870,6 +874,7 @@ def rope_turns(rot, base=10000.0, scaling=None, factor=1.0, original=None, low=1
     if scaling == "linear":
         f = f / factor
     elif scaling in ("wavelength", "ramp"):
+        high = (32.0 if scaling == "ramp" else 4.0) if high is None else high
         if not original or original <= 0 or not high > low:
             raise ValueError("scaling %r needs original > 0 and high > low" % scaling)
         if scaling == "wavelength":

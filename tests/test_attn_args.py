@@ -44,3 +44,21 @@ def test_factors_that_are_no_numbers(L, mscale):
     st = A.strides(*[8] * 6)
     assert L.kv_append(A.P, A.P, None, None, st, A.P, A.P, A.P, A.P, A.P, None, r, A.shape(), None) == A.E_ARG
     assert b"mscale" in L.fc_last_error()
+
+
+def test_ramp_without_bounds_takes_its_own():
+    """The blend by index runs from 32 turns to 1 unless told otherwise, the one by
+    wavelength from 4 to 1."""
+    kw = dict(rot=64, factor=8.0, original=4096)
+    for kind, high in (("ramp", 32.0), ("wavelength", 4.0)):
+        t, m = fc.rope_turns(scaling=kind, **kw)
+        want, mw = fc.rope_turns(scaling=kind, low=1.0, high=high, **kw)
+        assert torch.equal(t, want) and m == mw
+        other, _ = fc.rope_turns(scaling=kind, low=1.0, high=36.0 - high, **kw)
+        assert not torch.equal(t, other)
+    # from the formula: 32 turns within 4096 positions are reached at pair 32 ln(4096 / (64 pi)) / ln 10000
+    # = 10.47, one at 22.51: pairs to 10 stay, pairs from 23 on are divided, pair 17 is 7 / 13 of the way
+    t, plain = fc.rope_turns(scaling="ramp", **kw)[0], fc.rope_turns(64)[0]
+    part = [int(a) / int(b) for a, b in zip(t, plain)]
+    assert all(abs(p - 1) < 1e-9 for p in part[:11]) and all(abs(p - 0.125) < 1e-9 for p in part[23:])
+    assert abs(part[17] - (1 - 7 / 13 * 0.875)) < 1e-9
