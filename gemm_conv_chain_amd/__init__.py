@@ -820,6 +820,14 @@ def _exact(t, name, shape, dtype):
         raise ValueError("%s must be contiguous with shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
+def _dense(table):
+    """table, or a copy of it if it is a slice of a wider one: a row ends where the
+    slice ends, which the C entry points cannot be told apart from a row's stride."""
+    if isinstance(table, _torch().Tensor) and not table.is_contiguous():
+        return table.contiguous()
+    return table
+
+
 def _one_device(dev, tensors):
     """Every tensor (None: absent) sits on device `dev`."""
     if dev < 0:
@@ -965,7 +973,8 @@ def kv_append(k, v, codes, scales, table, cu_q, kv_lens, turns=None, interleaved
     """Append k, v [tokens, hkv, d] to the paged cache (codes, scales), k turned by
     the rotary table ``turns`` on the way (None: as it is).  Sequence b's new tokens
     are rows cu_q[b]:cu_q[b+1] and the last of its kv_lens[b] tokens; slot s is in
-    page table[b, s // page].  ``positions`` (int32 [tokens]) turn instead of the slots.
+    page table[b, s // page] (a table that is a slice of a wider one is copied, one
+    small launch).  ``positions`` (int32 [tokens]) turn instead of the slots.
     With ``q`` [tokens, hq, d] the same launch returns q turned alike (``q_out``).
     ``max_q``: a bound of the new tokens of a sequence; it sizes the launch."""
     dt = _rows(k, "k")
@@ -984,6 +993,7 @@ def kv_append(k, v, codes, scales, table, cu_q, kv_lens, turns=None, interleaved
             _exact(q_out, "q_out", q.shape, q.dtype)
     elif q_out is not None:
         raise ValueError("q_out needs q")
+    table = _dense(table)
     sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, None)
     rt = _table(turns, interleaved, mscale)
     if positions is not None:
@@ -1007,6 +1017,7 @@ def kv_check(table, cu_q, kv_lens, pages, page, tokens=None, writes=False):
     sequences name).  On the device such faults give NaN rows."""
     torch = _torch()
     B, stride = _ndim(table, "table", 2)
+    table = _dense(table)
     for t, name, shape in ((table, "table", (B, stride)), (cu_q, "cu_q", (B + 1,)), (kv_lens, "kv_lens", (B,))):
         if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.is_cuda:
             raise TypeError("%s must be a host tensor of torch.int32" % name)
@@ -1052,6 +1063,7 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     dt = _rows(q, "q")
     T, hq, d = shape = q.shape
     hkv = _ndim(codes, "codes", 5)[1]
+    table = _dense(table)
     sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv)
     pa = _attn_params(d, scale, causal, softcap, window, variant, splits)
     if slopes is not None:

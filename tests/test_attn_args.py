@@ -62,3 +62,23 @@ def test_ramp_without_bounds_takes_its_own():
     part = [int(a) / int(b) for a, b in zip(t, plain)]
     assert all(abs(p - 1) < 1e-9 for p in part[:11]) and all(abs(p - 0.125) < 1e-9 for p in part[23:])
     assert abs(part[17] - (1 - 7 / 13 * 0.875)) < 1e-9
+
+
+def test_table_slices_are_taken():
+    """A table that is a slice of a wider one (host tensors: only what is refused
+    after it is)."""
+    kw = A.host()
+    q = kw.pop("q")
+    wide = torch.zeros((2, 9), dtype=torch.int32)
+    for table in (wide[:, :2], wide[:, 3:5], torch.zeros((2, 2), dtype=torch.int32).t()):
+        with pytest.raises(TypeError, match="device"):
+            fc.chain_attn(q, **{**kw, "table": table})
+        with pytest.raises(TypeError, match="device"):
+            fc.kv_append(q[:, :2], q[:, :2], **{**kw, "table": table})
+    with pytest.raises(TypeError, match="table"):
+        fc.chain_attn(q, **{**kw, "table": wide.long()[:, :2]})
+    cu, lens = A.i32([0, 2, 3]), A.i32([40, 32])
+    t = A.i32([[9, 0, 1, 2, 9], [9, 3, 4, -1, 9]])
+    fc.kv_check(t[:, 1:4], cu, lens, pages=5, page=16, writes=True)
+    with pytest.raises(fc.FusedChainError, match=r"table\[1\]\[1\] = 4"):
+        fc.kv_check(t[:, 1:4], cu, lens, pages=4, page=16)
