@@ -136,16 +136,21 @@ int64_t key_blocks(const fc_kv_shape* s, const fc_attn_params* p, int64_t rows)
 //   + 20 + 2 n * tokens * hq * d / 10^6, if n > 1                           partial results and join
 // where chunk is in blocks of 16 keys, tiles are those that `tokens` fill (fewer
 // than max_q allows if the batch is ragged), and a CU does the work of k = 1.5 (d =
-// 64: of three at a time), 2 (d = 128) or 1.5 tiles in the time of one.  More splits
-// have to gain 4 %.  The numbers are fits to 80 drawn calls (d = 64 to 256, 1 to 16
-// sequences, to 32768 keys, most of them ragged) timed with 1 to 16 splits: the choice
-// is 4 % from the best on average and 1.5 times it at worst; filling the machine once,
-// by max_q, was 14 % and 2.1 times.  (us, by splits, the choice marked:)
+// 64), 2 (d = 128) or 1.5 tiles in the time of one.  More splits have to gain 4 %.  The
+// numbers are fits to 80 drawn calls (d = 64 to 256, 1 to 16 sequences, to 32768 keys,
+// most of them ragged) timed with 1 to 16 splits: the choice is 4 % from the best on
+// average and 1.5 times it at worst; filling the machine once, by max_q, was 14 % and
+// 2.1 times.  (us, by splits, the choice marked:)
 //   d = 64, 138 tiles of 8000 keys, ragged      1: 122   2: 86   4: 70    6*: 59   8: 70
 //   d = 64, 584 tiles of 12001 keys             1: 511   2*: 420  4: 386   8: 434
 //   d = 128, 346 tiles of 4000 keys, ragged     1*: 110   2: 147   4: 141
 //   d = 64, 62 tiles of 16000 keys, ragged      1: 238   4: 75   8: 55   10: 68   (9 taken)
 //   d = 256, 8 tiles of 14400 keys              1: 890   4: 246   16: 87          (29 taken)
+// One k serves all kinds of scores, though at d = 64 a CU holds three tiles of plain or
+// capped ones and two with a bias (below, 496 blocks with keys at three splits: one
+// round of either; four splits are one round of plain ones, and two with a bias):
+//   4 chunks of 515 queries, 12001 keys, ragged 1: 198   2: 125   3*: 120  4: 102  6: 118
+//   with a bias                                 1: 242   2: 149   3*: 113  4: 153  6: 122
 int64_t tile_splits(const fc_kv_shape* s, int64_t per, int64_t base, int64_t blocks)
 {
     const double rows = (double)s->tokens * (s->hq / s->hkv);

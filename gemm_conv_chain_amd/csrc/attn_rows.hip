@@ -19,9 +19,12 @@
 // way.  The keys are split over a block's waves, and over blocks where
 // sequences x heads alone do not fill the machine; the waves' results are
 // joined through LDS and the blocks' by k_attn_join, both in a fixed order.
-// Measured: 64 sequences x 8 kv heads of 128, to 8192 keys, 756 MB in 127 us (5.9
-// TB/s); 2 x 4, 131071 keys, 269 MB in 53 us with the join; 24 x 16 heads of 256,
-// three tokens, a window of 4096, 786 MB in 135 us (5.8 TB/s).
+// Measured: 64 sequences x 8 kv heads of 128, to 8192 keys, 756 MB in 127 to 133 us
+// (5.7 to 5.9 TB/s); 2 x 4, 131071 keys, 269 MB in 53 us with the join; 24 x 16 heads
+// of 256, three tokens, a window of 4096, 786 MB in 135 to 141 us (5.6 to 5.8 TB/s).
+// 17 to 32 rows with heads of 256 are far from that: two column tiles beside 64 keys
+// of K and V take all 512 registers, 65 to 73 are spilled, and 24 sequences of up to
+// 9000 keys x 8 heads, 24 rows each, take 216 us for 594 MB (2.7 TB/s).
 #include "fc_launch.h"
 #include "kv_common.h"
 

@@ -20,9 +20,15 @@
 // cycles of matrix instructions and about 800 of vector ones (32 exponentials, at
 // 8 cycles, are a third of these), two waves a SIMD fill each other's gaps, and
 // the clock sinks under the load.  Measured for two prompts of 4096 with 32 query
-// heads of 128: 271 to 289 us by box (950 to 1015 TFLOP/s; a library product of
-// 8192^3 reaches 1170); without the exponentials, the widening and the maximum
-// the same loop still takes 227.
+// heads of 128: 271 to 304 us by card (906 to 1015 TFLOP/s; a library product of
+// 8192^3 reaches 1170 to 1300); without the exponentials, the widening and the
+// maximum the same loop still takes 227.  Two prompts of 4096 with other heads: 32
+// of 64, where the vector pipe is the longer one, 188 to 198 us; with a cap 253 to
+// 276 (three slow operations a score for one), with a bias 214 to 229 (172 registers
+// leave a SIMD two waves, plain and capped scores three); 16 of 192 217 to 226; 16 of
+// 256 318 to 347 (queries and accumulators are 192 of 256 registers, 25 to 40 are
+// spilled); 32 of 128 with a cap 351 to 367.  lse takes every exponential twice: 352
+// us against 293 (d = 128), 152 against 120 for chunks with a bias.
 #include "fc_launch.h"
 #include "kv_common.h"
 

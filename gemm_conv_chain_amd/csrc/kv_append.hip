@@ -14,8 +14,9 @@
 // bits of a mask in LDS).  Waves 0 .. WPS - 1 take K, the next WPS take V.
 //
 // Bound by memory for prompts: six of them, 20 k tokens, 32 query heads, 8 kv
-// heads of 128: 499 MB in 112 us (4.4 TB/s; a copy reaches 4.8).  A step's token
-// is a chain of loads (lengths, page, values, scale): 8 us for 128 sequences.
+// heads of 128: 499 MB in 112 us (4.4 TB/s; a copy of as many bytes takes 94).  A
+// step's token is a chain of loads (lengths, page, values, scale): 8 us for 128
+// sequences.
 #include "fc_launch.h"
 #include "kv_common.h"
 

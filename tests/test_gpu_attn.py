@@ -41,8 +41,8 @@ def i32(v):
     (33, 5, 192, 48, False, 1.25),
     (5, 2, 256, 16, True, 1.0),
     (19, 9, 80, 80, False, 1.0),
-    (700, 40, 128, 128, False, 1.0),      # enough for four heads a thread, 40 = 10 * 4
-    (900, 35, 128, 96, True, 0.5),        # and with three left over
+    (700, 40, 128, 128, False, 1.0),      # many blocks
+    (900, 35, 128, 96, True, 0.5),        # and an odd number of heads
 ])
 def test_rope(fc, dtype, interleaved, T, H, D, rot, inverse, mscale):
     print("case rope", dtype, interleaved, T, H, D, rot, inverse, flush=True)
