@@ -14,17 +14,24 @@ The functions mirror the C entry points:
 * ``rope(x, positions, turns)``, ``kv_append(k, v, codes, ...)``,
   ``chain_attn(q, codes, ...)``   rotary positions, appending to a paged cache of
   8-bit codes (``kv_cache``), and attention over it (softmax(q K^T) V as a chain)
+* ``tree_plan(parents, ...)``, ``chain_attn(..., tree=...)``, ``sample_tokens(logits,
+  u)``, ``tree_accept(...)``, ``kv_keep(...)``   a step that verifies drafted tokens;
+  ``kv_copy`` and ``KvPages`` copy, fork, pack and free the cache's pages
 * ``pad_channels`` / ``pad_weight_channels``   zero padding of channel counts
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
+import heapq
+import itertools
 import math
 import os
 import re
 
 __all__ = ["DTYPE", "ATTN_VARIANT", "rope_turns", "rope", "kv_cache", "kv_append", "kv_check", "chain_attn", "attn_plan",
+           "tree_plan", "tree_accept", "kv_keep", "kv_copy", "KvPages", "sample_tokens",
            "TuneEntry", "tune_chain_gemm2_table", "auto_config", "tune_conv_pool", "conv_auto_config", "CONV_VARIANT", "lib", "FusedChainError", "chain_gemm2", "tune_chain_gemm2", "auto_variant", "tune_clear", "chain_gemmN", "chain_conv_pool", "chain_conv_bn_pool", "chain_conv2", "chain_convN", "convN_auto_variant", "tune_chain_convN",
            "gemm_bias_act", "conv_bias_act", "maxpool2x2", "avgpool2x2", "pad_channels", "pad_weight_channels", "abi_version", "ACT", "VARIANT",
            "LIB_PATH", "POISON_LIB_PATH", "poison_build", "HEADER_PATH", "exported_names"]
@@ -81,6 +88,17 @@ class AttnParams(ctypes.Structure):
 class AttnPlan(ctypes.Structure):
     _fields_ = [("variant", ctypes.c_int32), ("splits", ctypes.c_int32), ("chunk", ctypes.c_int32),
                 ("workspace", ctypes.c_int64)]
+
+
+class Tree(ctypes.Structure):
+    """fc_tree: what the new tokens of a tree see of each other, and where they sit."""
+    _fields_ = [("bits", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("words", ctypes.c_int32)]
+
+
+class Sampling(ctypes.Structure):
+    """fc_sampling: arrays of a row's settings (or NULL), and the values for all rows."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("temperatures", "top_ks", "top_ps", "min_ps")] + [
+        ("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)]
 
 
 _lib = None
@@ -189,9 +207,18 @@ def _load(path):
     L.chain_attn.argtypes = [_vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(AttnParams), _vp,
                              _vp, ctypes.POINTER(KvShape), _vp, _i64, _vp]
     L.kv_check.argtypes = [_vp, _vp, _vp, ctypes.POINTER(KvShape), _i32]
+    L.chain_attn_tree.argtypes = [_vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(Tree), _vp,
+                                  ctypes.POINTER(AttnParams), _vp, _vp, ctypes.POINTER(KvShape), _vp, _i64, _vp]
+    L.tree_plan.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp]
+    L.tree_accept.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp]
+    L.kv_keep.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, ctypes.POINTER(KvShape), _vp]
+    L.kv_copy.argtypes = [_vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _vp]
+    L.sample_workspace.argtypes = [_i32, _i64, _i32, ctypes.POINTER(_i64)]
+    L.sample_tokens.argtypes = [_vp, _i32, _i64, _i32, _i64, _vp, ctypes.POINTER(Sampling), _vp, _vp, _i64, _vp]
     L.fc_tune_clear.restype = None
     L.fc_tune_clear.argtypes = []
-    for name in ("rope_apply", "kv_append", "chain_attn_plan", "chain_attn", "kv_check", "chain_conv2_auto_config", "chain_conv2_ex", "chain_conv2_variant", "chain_conv2_tune", "winograd_weights", "chain_conv_pool_winograd", "chain_gemm2_ex", "chain_gemm2_tune_ex", "chain_gemm2_auto_config", "chain_conv_pool_tune",
+    for name in ("chain_attn_tree", "tree_plan", "tree_accept", "kv_keep", "kv_copy", "sample_workspace", "sample_tokens",
+                 "rope_apply", "kv_append", "chain_attn_plan", "chain_attn", "kv_check", "chain_conv2_auto_config", "chain_conv2_ex", "chain_conv2_variant", "chain_conv2_tune", "winograd_weights", "chain_conv_pool_winograd", "chain_gemm2_ex", "chain_gemm2_tune_ex", "chain_gemm2_auto_config", "chain_conv_pool_tune",
                  "chain_conv_pool_auto_config", "chain_conv_pool_ex", "avgpool2x2", "fc_probe_mfma", "fc_probe_read", "chain_conv_bn_pool", "chain_convN", "chain_convN_variant", "chain_convN_auto_variant", "chain_convN_tune", "chain_gemm2_tune", "chain_gemm2_auto_variant", "chain_gemm2", "chain_gemm2_variant", "chain_gemmN", "chain_conv_pool", "chain_conv2", "gemm_bias_act",
                  "conv_bias_act", "maxpool2x2", "pad_channels"):
         getattr(L, name).restype = ctypes.c_int
@@ -844,6 +871,15 @@ def _raw_stream(dev):
     return _torch()._C._cuda_getCurrentRawStream(dev)
 
 
+def _call(dev, f, *args):
+    """f(*args) with device `dev`, whose stream the call names, as the current one."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == dev:
+        return f(*args)
+    with torch.cuda.device(dev):
+        return f(*args)
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -1048,8 +1084,22 @@ def attn_plan(tokens, batch, hq, hkv, d, page, table_stride, max_q, max_kv, dtyp
             "workspace": int(plan.workspace)}
 
 
+def _tree(tree, tokens):
+    """(fc_tree, bits, positions) of the pair that ``tree_plan`` returns."""
+    torch = _torch()
+    if tree is None:
+        return None, None, None
+    if not isinstance(tree, (tuple, list)) or len(tree) != 2:
+        raise TypeError("tree must be the pair (bits, positions), got %s" % type(tree).__name__)
+    bits, positions = tree
+    words = _ndim(bits, "the tree's bits", 2)[1]
+    _exact(bits, "the tree's bits", (tokens, words), torch.int64)
+    _exact(positions, "the tree's positions", (tokens,), torch.int32)
+    return Tree(bits.data_ptr(), positions.data_ptr(), words), bits, positions
+
+
 def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, softcap=0.0, window=0, slopes=None,
-               max_q=None, max_kv=None, out=None, lse=None, workspace=None, variant="auto", splits=0):
+               max_q=None, max_kv=None, out=None, lse=None, workspace=None, variant="auto", splits=0, tree=None):
     """out [tokens, hq, d] = softmax(scale * q K^T) V over the paged cache: queries
     cu_q[b]:cu_q[b+1] are the last of sequence b's kv_lens[b] tokens and, if ``causal``,
     see the slots up to their own (the last ``window`` of them if window > 0).
@@ -1060,7 +1110,10 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     (they size the launch; give ``max_q`` for steps: None takes all the tokens for one
     sequence's, and 64 single queries over 8192 keys take 290 us rather than 127);
     ``workspace``: uint8 device memory of attn_plan's size
-    (allocated if None); ``variant``, ``splits``: kernel form and split, by rule if not given."""
+    (allocated if None); ``variant``, ``splits``: kernel form and split, by rule if not given.
+    ``tree``: the new tokens are nodes of a tree of drafts, (bits, positions) as ``tree_plan``
+    returns them: a node sees every slot before its sequence's first node and the nodes of
+    its bits; ``window`` and ``slopes`` go by the positions."""
     torch = _torch()
     dt = _rows(q, "q")
     T, hq, d = shape = q.shape
@@ -1068,6 +1121,7 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     table = _dense(table)
     sh = _kv_shape(dt, T, hq, hkv, d, codes, scales, table, cu_q, kv_lens, max_q, max_kv)
     pa = _attn_params(d, scale, causal, softcap, window, variant, splits)
+    tr, bits, positions = _tree(tree, T)
     if slopes is not None:
         _exact(slopes, "slopes", (hq,), torch.float32)
     if out is not None:
@@ -1078,7 +1132,7 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
         raise TypeError("workspace must be contiguous torch.uint8")
     dev = q.get_device()
-    _one_device(dev, (codes, scales, table, cu_q, kv_lens, slopes, out, le, workspace))
+    _one_device(dev, (codes, scales, table, cu_q, kv_lens, slopes, out, le, workspace, bits, positions))
     L = lib()
     plan = AttnPlan()
     s = L.chain_attn_plan(sh, pa, plan)
@@ -1093,9 +1147,347 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
         room = workspace.numel()
     elif room:
         workspace = torch.empty(room, dtype=torch.uint8, device=q.device)
-    s = L.chain_attn(q.data_ptr(), _STRIDES[2](q.stride(0), q.stride(1)), codes.data_ptr(), scales.data_ptr(),
-                     table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), _addr(slopes), pa, out.data_ptr(), _addr(le), sh,
-                     _addr(workspace), room, _raw_stream(dev))
+    st = _STRIDES[2](q.stride(0), q.stride(1))
+    if tr is None:
+        s = _call(dev, L.chain_attn, q.data_ptr(), st, codes.data_ptr(), scales.data_ptr(), table.data_ptr(), cu_q.data_ptr(),
+                  kv_lens.data_ptr(), _addr(slopes), pa, out.data_ptr(), _addr(le), sh, _addr(workspace), room,
+                  _raw_stream(dev))
+    else:
+        s = _call(dev, L.chain_attn_tree, q.data_ptr(), st, codes.data_ptr(), scales.data_ptr(), table.data_ptr(),
+                  cu_q.data_ptr(), kv_lens.data_ptr(), tr, _addr(slopes), pa, out.data_ptr(), _addr(le), sh,
+                  _addr(workspace), room, _raw_stream(dev))
     if s:
         _check("chain_attn", s)
     return (out, le) if le is not None else out
+
+
+# -------------------------------------------------- trees of drafted tokens
+def _indices(tensors, shape):
+    for t, name in tensors:
+        _exact(t, name, shape, _torch().int32)
+
+
+def _bound(max_q, tokens):
+    """A bound of the nodes of a tree that a row of bits or of kept nodes holds."""
+    n = tokens if max_q is None else int(max_q)
+    if n > 4096:
+        if max_q is not None:
+            raise ValueError("max_q must be at most 4096, got %d" % n)
+        n = 4096
+    return max(n, 1)
+
+
+def tree_plan(parents, cu_q, kv_lens, max_q=None):
+    """(bits int64 [tokens, ceil(max_q / 64)], positions int32 [tokens]) of trees of new
+    tokens, for ``chain_attn(tree=...)`` and ``kv_append(positions=...)``: once a step, for all
+    layers.  ``parents`` (int32 [tokens]): each token's parent among its sequence's new ones,
+    an earlier one, or -1.  A token sees its ancestors and itself, and sits its depth past
+    what the sequence held before.  ``max_q``: a bound of the new tokens of a sequence, at
+    most 4096 (sequences past it get NaN rows)."""
+    torch = _torch()
+    T, = _ndim(parents, "parents", 1)
+    B, = _ndim(kv_lens, "kv_lens", 1)
+    _indices(((parents, "parents"),), (T,))
+    _indices(((kv_lens, "kv_lens"),), (B,))
+    _indices(((cu_q, "cu_q"),), (B + 1,))
+    words = -(-_bound(max_q, T) // 64)
+    dev = parents.get_device()
+    _one_device(dev, (cu_q, kv_lens))
+    bits = torch.empty((T, words), dtype=torch.int64, device=parents.device)
+    positions = torch.empty_like(parents)
+    s = _call(dev, lib().tree_plan, parents.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), B, T, words, bits.data_ptr(),
+              positions.data_ptr(), _raw_stream(dev))
+    if s:
+        _check("tree_plan", s)
+    return bits, positions
+
+
+def tree_accept(parents, drafted, targets, cu_q, kv_lens, max_q=None):
+    """(keep [batch, max_q], kept [batch], next [batch], lens [batch]), all int32: each tree
+    walked from node 0, the token that the last step decided, to the first child whose
+    ``drafted`` token is the one that ``targets`` holds for the present node (the model's own
+    choice there, of ``sample_tokens``), until there is none.  ``keep``: the nodes passed, rising,
+    -1 behind them; ``kept``: how many; ``next``: the target of the last; ``lens``: the
+    sequence's length with them."""
+    torch = _torch()
+    T, = _ndim(parents, "parents", 1)
+    B, = _ndim(kv_lens, "kv_lens", 1)
+    _indices(((parents, "parents"), (drafted, "drafted"), (targets, "targets")), (T,))
+    _indices(((kv_lens, "kv_lens"),), (B,))
+    _indices(((cu_q, "cu_q"),), (B + 1,))
+    most = _bound(max_q, T)
+    dev = parents.get_device()
+    _one_device(dev, (drafted, targets, cu_q, kv_lens))
+    out = torch.empty((B, most + 3), dtype=torch.int32, device=parents.device).view(-1)
+    keep, kept, nxt, lens = (out[:B * most].view(B, most), out[B * most:B * (most + 1)], out[B * (most + 1):B * (most + 2)],
+                             out[B * (most + 2):])
+    s = _call(dev, lib().tree_accept, parents.data_ptr(), drafted.data_ptr(), targets.data_ptr(), cu_q.data_ptr(),
+              kv_lens.data_ptr(), B, T, most, keep.data_ptr(), kept.data_ptr(), nxt.data_ptr(), lens.data_ptr(),
+              _raw_stream(dev))
+    if s:
+        _check("tree_accept", s)
+    return keep, kept, nxt, lens
+
+
+def _pool(codes, scales):
+    """(layers, pages, hkv, page, d) of a pool, one layer's or [layers, ...] of several."""
+    torch = _torch()
+    shape = _ndim(codes, "codes", None)
+    if len(shape) not in (5, 6):
+        raise ValueError("codes must have 5 dims, or 6 with layers, got shape %s" % (shape,))
+    _exact(codes, "codes", codes.shape, torch.uint8)
+    L = shape[0] if len(shape) == 6 else 1
+    P, H, two, n, w = shape[-5:]
+    if two != 2 or w % 16:
+        raise ValueError("codes must have shape ([layers,] pages, hkv, 2, page / 16, 16 d), got %s" % (shape,))
+    _exact(scales, "scales", codes.shape[:-2], torch.float32)
+    return L, P, H, 16 * n, w // 16
+
+
+def kv_keep(codes, scales, table, cu_q, kv_lens, keep, kept):
+    """Of each sequence's new tokens in the cache (the last cu_q[b + 1] - cu_q[b] of kv_lens[b]),
+    those that ``keep`` (int32 [batch, n], rising) names, ``kept`` (int32 [batch]) of them, move to
+    the front: slots kv_lens[b] - new + i.  ``codes`` and ``scales`` may be one layer's or
+    [layers, ...] of all that share the table.  A page's scale becomes the largest of its own
+    and its tokens' pages'.  A sequence whose list is not rising stays as it is.  The lengths
+    do not change: ``tree_accept`` returns the new ones."""
+    torch = _torch()
+    L, P, H, page, d = _pool(codes, scales)
+    table = _dense(table)
+    B, stride = shape = _ndim(table, "table", 2)
+    _indices(((table, "table"),), shape)
+    _indices(((cu_q, "cu_q"),), (B + 1,))
+    _indices(((kv_lens, "kv_lens"), (kept, "kept")), (B,))
+    most = _ndim(keep, "keep", 2)[1]
+    _indices(((keep, "keep"),), (B, most))
+    dev = codes.get_device()
+    _one_device(dev, (scales, table, cu_q, kv_lens, keep, kept))
+    sh = KvShape(0, B, H, H, d, page, P, stride, 0x3fffffff // max(H, 1), 0, 0)
+    s = _call(dev, lib().kv_keep, codes.data_ptr(), scales.data_ptr(), L, table.data_ptr(), cu_q.data_ptr(),
+              kv_lens.data_ptr(), keep.data_ptr(), kept.data_ptr(), most, sh, _raw_stream(dev))
+    if s:
+        _check("kv_keep", s)
+
+
+def kv_copy(codes, scales, pairs):
+    """Pages of the pool to others, codes and scales: ``pairs`` is a list of (from, to) or a host
+    tensor int32 [n, 2], checked before anything is copied: ids inside the pool, no page the
+    destination of two, none a source and a destination.  ``codes`` and ``scales`` may be one
+    layer's or [layers, ...]."""
+    torch = _torch()
+    L, P, H, page, d = _pool(codes, scales)
+    if isinstance(pairs, torch.Tensor):
+        n = _ndim(pairs, "pairs", 2)[0]
+        if pairs.is_cuda:
+            raise TypeError("pairs must be on the host")
+        _exact(pairs, "pairs", (n, 2), torch.int32)
+        at = pairs.data_ptr()
+    else:
+        pairs = list(pairs)
+        n = len(pairs)
+        if any(len(p) != 2 for p in pairs):
+            raise ValueError("pairs must be of two pages each")
+        pairs = array.array("i", itertools.chain.from_iterable(pairs))
+        at = pairs.buffer_info()[0]
+    dev = codes.get_device()
+    _one_device(dev, (scales,))
+    s = _call(dev, lib().kv_copy, codes.data_ptr(), scales.data_ptr(), L, P, H, page, d, at, n, _raw_stream(dev))
+    if s:
+        _check("kv_copy", s)
+
+
+# ------------------------------------------------------------ drawing tokens
+_LOGITS = {}   # torch dtype -> C code
+
+
+def _setting(v, name, rows, dtype):
+    """(address or None, value, tensor or None) of a row's setting."""
+    torch = _torch()
+    if isinstance(v, torch.Tensor):
+        _exact(v, name, (rows,), dtype)
+        return v.data_ptr(), 0, v
+    return None, v, None
+
+
+def sample_tokens(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, workspace=None):
+    """One token (int32 [rows]) drawn from each row of ``logits`` [rows, vocab] (float16,
+    bfloat16 or float32, a row's logits adjacent) by the random numbers ``u`` (float32
+    [rows], in [0, 1)).  Weights are exp((x - max) / temperature).  In falling order, equal
+    logits by index, a token stays if it is among the first ``top_k`` (0: all), the weights
+    before it are under ``top_p`` of what top_k left, and its own is at least ``min_p`` of the
+    largest; the first always stays.  Of these the first token in order of index is drawn at
+    which the running sum of weights exceeds u times their sum.  Temperature 0 takes the
+    first of the falling order.  Each setting is a number or a device tensor [rows] (float32,
+    top_k int32).  A row with a NaN or +inf, or of -inf alone, gives -1.  ``workspace``: uint8
+    device memory (allocated if None)."""
+    torch = _torch()
+    if not _LOGITS:
+        _LOGITS.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    dt = _LOGITS.get(getattr(logits, "dtype", None))
+    if dt is None:
+        raise TypeError("logits must be a torch tensor of float16, bfloat16 or float32, got %s"
+                        % (getattr(logits, "dtype", type(logits).__name__),))
+    R, V = _ndim(logits, "logits", 2)
+    if logits.stride(1) != 1 and V > 1:
+        raise ValueError("the logits of a row must be adjacent")
+    f32 = torch.float32
+    _exact(u, "u", (R,), f32)
+    ta, t, tt = _setting(temperature, "temperature", R, f32)
+    ka, k, kt = _setting(top_k, "top_k", R, torch.int32)
+    pa, p, pt = _setting(top_p, "top_p", R, f32)
+    ma, m, mt = _setting(min_p, "min_p", R, f32)
+    if not -1 <= k <= 0x7fffffff:      # (ctypes would keep the low 32 bits)
+        k = 0x7fffffff if k > 0 else -1
+    if out is not None:
+        _exact(out, "out", (R,), torch.int32)
+    if workspace is not None and (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()):
+        raise TypeError("workspace must be contiguous torch.uint8")
+    dev = logits.get_device()
+    _one_device(dev, (u, tt, kt, pt, mt, out, workspace))
+    L = lib()
+    need = _i64()
+    s = L.sample_workspace(dt, R, V, need)
+    if s:
+        _check("sample_tokens", s)
+    room = need.value
+    if workspace is not None:
+        room = workspace.numel()
+    elif room:
+        workspace = torch.empty(room, dtype=torch.uint8, device=logits.device)
+    if out is None:
+        out = torch.empty(R, dtype=torch.int32, device=logits.device)
+    s = _call(dev, L.sample_tokens, logits.data_ptr(), dt, R, V, logits.stride(0), u.data_ptr(),
+              Sampling(ta, ka, pa, ma, t, k, p, m), out.data_ptr(), _addr(workspace), room, _raw_stream(dev))
+    if s:
+        _check("sample_tokens", s)
+    return out
+
+
+# ------------------------------------------------------------- pages (host)
+class KvPages:
+    """Hands out a pool's pages on the host: which sequence (any hashable name) holds which
+    page, and how many hold it.  Pages that a fork shares are copied before the one that
+    writes gets them.  Nothing here touches the device: what has to be copied there is
+    returned as pairs for ``kv_copy``, to be run before the next call here and before what
+    the pages are grown for is written.
+
+        pages.fork("a", "b")                                  # b continues a: its pages are shared
+        kv_copy(codes, scales, pages.grow("b", new_length))   # room for b's next tokens
+        table = pages.table(["a", "b"])                       # host int32, a row a sequence
+    """
+
+    def __init__(self, pages, page):
+        if pages < 0 or page < 16 or page % 16:
+            raise ValueError("pages >= 0 and a page of a multiple of 16 tokens required")
+        self.page = int(page)
+        self.refs = [0] * int(pages)
+        self._free = list(range(int(pages)))   # a heap: the lowest page first
+        self._rows = {}
+        self._lens = {}
+
+    @property
+    def available(self):
+        """Pages that nobody holds."""
+        return len(self._free)
+
+    def length(self, seq):
+        return self._lens[seq]
+
+    def held(self, seq):
+        """The pages of a sequence, in order of its tokens."""
+        return list(self._rows[seq])
+
+    def add(self, seq):
+        """A sequence without tokens."""
+        if seq in self._rows:
+            raise ValueError("sequence %r is there already" % (seq,))
+        self._rows[seq], self._lens[seq] = [], 0
+
+    def _take(self, n):
+        if n > len(self._free):
+            raise MemoryError("%d pages are needed, %d are free" % (n, len(self._free)))
+        got = [heapq.heappop(self._free) for _ in range(n)]
+        for p in got:
+            self.refs[p] = 1
+        return got
+
+    def _drop(self, p):
+        self.refs[p] -= 1
+        if self.refs[p] == 0:
+            heapq.heappush(self._free, p)
+
+    def grow(self, seq, length):
+        """Room for the tokens up to ``length``; the pages that they are written to become the
+        sequence's own.  Returns the pairs to copy.  All or nothing: without enough free
+        pages MemoryError, and nothing has changed."""
+        row, now = self._rows[seq], self._lens[seq]
+        if length < now:
+            raise ValueError("sequence %r has %d tokens, cannot grow to %d" % (seq, now, length))
+        first = now // self.page                          # the first page that is written
+        shared = [i for i in range(first, min(len(row), -(-length // self.page))) if self.refs[row[i]] > 1]
+        more = max(0, -(-length // self.page) - len(row))
+        got = self._take(len(shared) + more)
+        pairs = []
+        for i in shared:
+            to = got.pop(0)
+            if i * self.page < now:                       # it holds tokens
+                pairs.append((row[i], to))
+            self._drop(row[i])
+            row[i] = to
+        row += got
+        self._lens[seq] = length
+        return pairs
+
+    def cut(self, seq, length):
+        """Forgets the tokens past ``length`` and frees the pages that only they needed."""
+        row = self._rows[seq]
+        if not 0 <= length <= self._lens[seq]:
+            raise ValueError("sequence %r has %d tokens, cannot be cut to %d" % (seq, self._lens[seq], length))
+        keep = -(-length // self.page)
+        for p in row[keep:]:
+            self._drop(p)
+        del row[keep:]
+        self._lens[seq] = length
+
+    def fork(self, seq, new):
+        """``new`` continues ``seq``: every page is shared, and a partly filled last one copied by
+        the ``grow`` of whoever writes to it first."""
+        if new in self._rows:
+            raise ValueError("sequence %r is there already" % (new,))
+        row = self._rows[seq]
+        for p in row:
+            self.refs[p] += 1
+        self._rows[new], self._lens[new] = list(row), self._lens[seq]
+
+    def free(self, seq):
+        """Forgets a sequence; pages that nobody else holds are free again."""
+        for p in self._rows.pop(seq):
+            self._drop(p)
+        del self._lens[seq]
+
+    def pack(self):
+        """Moves the pages in use to the front of the pool.  Returns the pairs to copy; tables made
+        before name the old places."""
+        used = [p for p, n in enumerate(self.refs) if n]
+        to = {}
+        holes = [p for p in range(len(used)) if not self.refs[p]]
+        for p in reversed(used):
+            if p < len(used):
+                break
+            to[p] = holes[len(to)]
+        for a, b in to.items():
+            self.refs[b], self.refs[a] = self.refs[a], 0
+        for row in self._rows.values():
+            row[:] = [to.get(p, p) for p in row]
+        self._free = list(range(len(used), len(self.refs)))
+        return list(to.items())
+
+    def table(self, seqs, width=None):
+        """Host int32 [len(seqs), width]: each sequence's pages, 0 behind them."""
+        torch = _torch()
+        rows = [self._rows[s] for s in seqs]
+        most = max([len(r) for r in rows], default=0)
+        width = max(most, 1) if width is None else int(width)
+        if most > width:
+            raise ValueError("a sequence has %d pages, the table %d" % (most, width))
+        return torch.tensor([r + [0] * (width - len(r)) for r in rows], dtype=torch.int32).view(len(rows), width)

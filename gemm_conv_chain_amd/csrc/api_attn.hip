@@ -1,12 +1,10 @@
 // api_attn.hip -- the C ABI of the attention-serving operators: validation on
 // the host before any HIP call, the choice of kernel form and split, launch.
-#include <stdarg.h>
-#include <stdio.h>
-
 #include <new>
 #include <vector>
 
 #include "../../include/fusedchain.h"
+#include "api_checks.h"
 #include "fc_launch.h"
 #include "kv_common.h"
 
@@ -18,28 +16,18 @@ hipError_t run_kv_append(int dtype, const void* k, const void* v, const void* q,
                          const int* positions, const KvShape& s, const RopeArgs& r, hipStream_t st);
 hipError_t run_attn_rows(int dtype, const AttnArgs& a, hipStream_t st);
 hipError_t run_attn_tile(int dtype, const AttnArgs& a, hipStream_t st);
+hipError_t run_attn_rows_tree(int dtype, const AttnArgs& a, hipStream_t st);
+hipError_t run_attn_tile_tree(int dtype, const AttnArgs& a, hipStream_t st);
+hipError_t run_kv_keep(uint8_t* codes, float* scales, int layers, const int* table, const int* cu_q, const int* kv_lens,
+                       const int* keep, const int* kept, int max_keep, const KvShape& s, hipStream_t st);
 hipError_t run_attn_join(int dtype, const AttnArgs& a, hipStream_t st);
 }  // namespace fc
 
 namespace {
 
-fc_status fail(fc_status s, const char* fmt, ...)
-{
-    char msg[256];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(msg, sizeof msg, fmt, ap);
-    va_end(ap);
-    return (fc_status)fc::api_fail(s, msg);
-}
-
-fc_status done(hipError_t e, const char* what)
-{
-    if (e != hipSuccess) return fail(FC_E_HIP, "%s: %s", what, hipGetErrorString(e));
-    return (fc_status)fc::api_fail(FC_OK, "");
-}
-
-bool aligned(const void* p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
+using fc::aligned;
+using fc::done;
+using fc::fail;
 
 fc_status check_strides(const int64_t* strides, int n)
 {
@@ -220,6 +208,74 @@ void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
     out->workspace = n > 1 ? s->tokens * s->hq * n * (s->d + 4) * 4 : 0;
 }
 
+// A tree's words and pairing with the scores' order; its pointers are looked at with the others.
+fc_status check_tree(const fc_tree* t, const fc_attn_params* p)
+{
+    if (t->words < 1 || t->words > FC_TREE_WORDS)
+        return fail(FC_E_UNSUPPORTED, "words=%d: 1 to %d are implemented", t->words, FC_TREE_WORDS);
+    if (!p->causal) return fail(FC_E_ARG, "a tree needs causal scores");
+    if (!aligned(t->bits, 8) || !aligned(t->positions, 4))
+        return fail(FC_E_ALIGN, "bits must be 8-byte, positions 4-byte aligned");
+    return FC_OK;
+}
+
+fc_status attn_call(const void* q, const int64_t* strides, const uint8_t* codes, const float* scales,
+                    const int32_t* table, const int32_t* cu_q, const int32_t* kv_lens, const fc_tree* tree,
+                    const float* slopes, const fc_attn_params* params, void* out, float* lse,
+                    const fc_kv_shape* shape, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    fc_status s = check_shape(shape);
+    if (s != FC_OK) return s;
+    if ((s = check_params(shape, params)) != FC_OK) return s;
+    if ((s = check_strides(strides, 2)) != FC_OK) return s;
+    if (tree && (s = check_tree(tree, params)) != FC_OK) return s;
+    if (nothing(shape)) return done(hipSuccess, "");
+    if (tree && (!tree->bits || !tree->positions)) return fail(FC_E_NULL, "the tree's bits and positions are required");
+    if (!q || !out) return fail(FC_E_NULL, "q and out are required");
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(slopes, 4) || !aligned(workspace, 16))
+        return fail(FC_E_ALIGN, "q, out and workspace must be 16-byte, lse and slopes 4-byte aligned");
+    if ((s = check_cache(shape, codes, scales, table, cu_q, kv_lens)) != FC_OK) return s;
+    fc_attn_plan p;
+    plan_attn(shape, params, &p);
+    if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace))
+        return fail(workspace ? FC_E_SHAPE : FC_E_NULL, "a workspace of %lld bytes is required, got %lld",
+                    (long long)p.workspace, (long long)workspace_bytes);
+    fc::AttnArgs a;
+    a.q = q;
+    a.q_ts = strides[0];
+    a.q_hs = strides[1];
+    a.codes = codes;
+    a.scales = scales;
+    a.table = table;
+    a.cu_q = cu_q;
+    a.kv_lens = kv_lens;
+    a.slopes = slopes;
+    a.out = out;
+    a.lse = lse;
+    a.part_o = (float*)workspace;
+    a.part_ml = p.splits > 1 ? (fc::floatx4*)(a.part_o + shape->tokens * shape->hq * p.splits * shape->d) : nullptr;
+    a.s = kv(shape);
+    a.G = shape->hq / shape->hkv;
+    a.causal = params->causal != 0;
+    a.window = params->window;
+    a.nsplit = p.splits;
+    a.chunk = p.chunk / 16;
+    a.pg_shift = __builtin_ctz((unsigned)shape->page) - 4;
+    a.scale = params->scale;
+    a.cap = params->softcap;
+    a.by_g = fc::FastDiv::make(a.G);
+    a.tree_bits = tree ? (const unsigned long long*)tree->bits : nullptr;
+    a.tree_pos = tree ? tree->positions : nullptr;
+    a.tree_words = tree ? tree->words : 0;
+    const bool tile = p.variant == FC_ATTN_TILE;
+    hipError_t e = tree ? (tile ? fc::run_attn_tile_tree(shape->dtype, a, (hipStream_t)stream)
+                                : fc::run_attn_rows_tree(shape->dtype, a, (hipStream_t)stream))
+                        : (tile ? fc::run_attn_tile(shape->dtype, a, (hipStream_t)stream)
+                                : fc::run_attn_rows(shape->dtype, a, (hipStream_t)stream));
+    if (e == hipSuccess && p.splits > 1) e = fc::run_attn_join(shape->dtype, a, (hipStream_t)stream);
+    return done(e, tree ? "chain_attn_tree" : "chain_attn");
+}
+
 }  // namespace
 
 extern "C" {
@@ -280,48 +336,37 @@ fc_status chain_attn(const void* q, const int64_t* strides, const uint8_t* codes
                      const fc_attn_params* params, void* out, float* lse, const fc_kv_shape* shape, void* workspace,
                      int64_t workspace_bytes, void* stream)
 {
+    return attn_call(q, strides, codes, scales, table, cu_q, kv_lens, nullptr, slopes, params, out, lse, shape, workspace,
+                     workspace_bytes, stream);
+}
+
+fc_status chain_attn_tree(const void* q, const int64_t* strides, const uint8_t* codes, const float* scales,
+                          const int32_t* table, const int32_t* cu_q, const int32_t* kv_lens, const fc_tree* tree,
+                          const float* slopes, const fc_attn_params* params, void* out, float* lse,
+                          const fc_kv_shape* shape, void* workspace, int64_t workspace_bytes, void* stream)
+{
+    if (!tree) return fail(FC_E_NULL, "tree is NULL");
+    return attn_call(q, strides, codes, scales, table, cu_q, kv_lens, tree, slopes, params, out, lse, shape, workspace,
+                     workspace_bytes, stream);
+}
+
+fc_status kv_keep(uint8_t* codes, float* scales, int32_t layers, const int32_t* table, const int32_t* cu_q,
+                  const int32_t* kv_lens, const int32_t* keep, const int32_t* kept, int32_t max_keep,
+                  const fc_kv_shape* shape, void* stream)
+{
     fc_status s = check_shape(shape);
     if (s != FC_OK) return s;
-    if ((s = check_params(shape, params)) != FC_OK) return s;
-    if ((s = check_strides(strides, 2)) != FC_OK) return s;
-    if (nothing(shape)) return done(hipSuccess, "");
-    if (!q || !out) return fail(FC_E_NULL, "q and out are required");
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(slopes, 4) || !aligned(workspace, 16))
-        return fail(FC_E_ALIGN, "q, out and workspace must be 16-byte, lse and slopes 4-byte aligned");
+    if (layers < 0) return fail(FC_E_SHAPE, "layers=%d is negative", layers);
+    if (layers > 65535) return fail(FC_E_UNSUPPORTED, "layers=%d exceeds 65535", layers);
+    if (max_keep < 0) return fail(FC_E_SHAPE, "max_keep=%d is negative", max_keep);
+    if (max_keep > 64 * FC_TREE_WORDS)
+        return fail(FC_E_UNSUPPORTED, "max_keep=%d exceeds %d", max_keep, 64 * FC_TREE_WORDS);
+    if (nothing(shape) || layers == 0 || max_keep == 0) return done(hipSuccess, "");
+    if (!keep || !kept) return fail(FC_E_NULL, "keep and kept are required");
+    if (!aligned(keep, 4) || !aligned(kept, 4)) return fail(FC_E_ALIGN, "keep and kept must be 4-byte aligned");
     if ((s = check_cache(shape, codes, scales, table, cu_q, kv_lens)) != FC_OK) return s;
-    fc_attn_plan p;
-    plan_attn(shape, params, &p);
-    if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace))
-        return fail(workspace ? FC_E_SHAPE : FC_E_NULL, "a workspace of %lld bytes is required, got %lld",
-                    (long long)p.workspace, (long long)workspace_bytes);
-    fc::AttnArgs a;
-    a.q = q;
-    a.q_ts = strides[0];
-    a.q_hs = strides[1];
-    a.codes = codes;
-    a.scales = scales;
-    a.table = table;
-    a.cu_q = cu_q;
-    a.kv_lens = kv_lens;
-    a.slopes = slopes;
-    a.out = out;
-    a.lse = lse;
-    a.part_o = (float*)workspace;
-    a.part_ml = p.splits > 1 ? (fc::floatx4*)(a.part_o + shape->tokens * shape->hq * p.splits * shape->d) : nullptr;
-    a.s = kv(shape);
-    a.G = shape->hq / shape->hkv;
-    a.causal = params->causal != 0;
-    a.window = params->window;
-    a.nsplit = p.splits;
-    a.chunk = p.chunk / 16;
-    a.pg_shift = __builtin_ctz((unsigned)shape->page) - 4;
-    a.scale = params->scale;
-    a.cap = params->softcap;
-    a.by_g = fc::FastDiv::make(a.G);
-    hipError_t e = p.variant == FC_ATTN_TILE ? fc::run_attn_tile(shape->dtype, a, (hipStream_t)stream)
-                                             : fc::run_attn_rows(shape->dtype, a, (hipStream_t)stream);
-    if (e == hipSuccess && p.splits > 1) e = fc::run_attn_join(shape->dtype, a, (hipStream_t)stream);
-    return done(e, "chain_attn");
+    return done(fc::run_kv_keep(codes, scales, layers, table, cu_q, kv_lens, keep, kept, max_keep, kv(shape), (hipStream_t)stream),
+                "kv_keep");
 }
 
 fc_status kv_check(const int32_t* table, const int32_t* cu_q, const int32_t* kv_lens, const fc_kv_shape* shape,

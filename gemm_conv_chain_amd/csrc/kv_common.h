@@ -322,7 +322,28 @@ struct AttnArgs {
     int pg_shift;                            // a page holds 2^pg_shift blocks of 16
     float scale, cap;
     FastDiv by_g;
+    // A tree of new tokens instead of causal order: which of its sequence's new tokens each sees, a
+    // bit each [tokens, tree_words], and their positions [tokens].
+    const unsigned long long* tree_bits;
+    const int* tree_pos;
+    int tree_words;
 };
+
+// The bits of the 64 nodes from `node` on (which may lie before the tree or past it).
+__device__ __forceinline__ unsigned long long tree_window(const unsigned long long* row, int words, int node)
+{
+    const int w = node >> 6, sh = node & 63;
+    const unsigned long long lo = (unsigned)w < (unsigned)words ? row[w] : 0;
+    const unsigned long long hi = (unsigned)(w + 1) < (unsigned)words ? row[w + 1] : 0;
+    return sh ? lo >> sh | hi << (64 - sh) : lo;
+}
+
+// The position of new token `at`, kept where a tree of a sequence's nq tokens can reach.
+__device__ __forceinline__ int tree_place(const AttnArgs& a, long at, int pos0, int kv_len)
+{
+    const int p = a.tree_pos[at];
+    return p < pos0 ? pos0 : p < kv_len ? p : kv_len - 1;
+}
 
 // The first key that a query at `pos` sees (no difference of the two leaves 32 bits,
 // whatever the window and for positions before 0 too).
@@ -382,6 +403,17 @@ template <class F> inline hipError_t by_kind(const AttnArgs& a, F&& f)
     switch (score_kind(a)) {
     case SC_PLAIN: return f(IntC<SC_PLAIN>{});
     case SC_BIAS: return f(IntC<SC_BIAS>{});
+    case SC_CAP: return f(IntC<SC_CAP>{});
+    case SC_FAR: return f(IntC<SC_FAR>{});
+    default: return f(IntC<SC_ANY>{});
+    }
+}
+
+// The same for a tree, whose keys are not in order of distance: a bias takes the general kind.
+template <class F> inline hipError_t by_tree_kind(const AttnArgs& a, F&& f)
+{
+    switch (score_kind(a)) {
+    case SC_PLAIN: return f(IntC<SC_PLAIN>{});
     case SC_CAP: return f(IntC<SC_CAP>{});
     case SC_FAR: return f(IntC<SC_FAR>{});
     default: return f(IntC<SC_ANY>{});

@@ -620,6 +620,138 @@ fc_status chain_attn(const void *q, const int64_t *strides, const uint8_t *codes
                      const fc_attn_params *params, void *out, float *lse, const fc_kv_shape *shape,
                      void *workspace, int64_t workspace_bytes, void *stream);
 
+/* ---- trees of drafted tokens -------------------------------------------------
+ *
+ * A step that verifies drafts appends several tokens a sequence at once: the
+ * nodes of a tree, each the continuation of its parent.  Sequence b's n new
+ * tokens are its nodes 0 .. n - 1; parents [tokens] (int32, device) names each
+ * one's parent among them, an earlier node; anything else counts as none, the
+ * node then follows what the sequence held before.  Node 0 is the token that
+ * the last step decided, the others are drafts.  A step is
+ *   tree_plan -> kv_append (positions), chain_attn_tree for every layer
+ *   -> sample_tokens -> tree_accept -> kv_keep for all layers.
+ * A tree has at most 64 * FC_TREE_WORDS nodes.
+ */
+#define FC_TREE_WORDS 64
+
+/* A tree as attention reads it: bits [tokens][words], bit j of a node's row (bit
+ * j % 64 of word j / 64) = it sees node j of its sequence; positions [tokens],
+ * the node's own, at least the first node's slot (taken into [that slot, the
+ * sequence's last one]).  Bits may be any, not only a tree's. */
+typedef struct {
+    const uint64_t *bits;
+    const int32_t *positions;
+    int32_t words;          /* 1 .. FC_TREE_WORDS; a sequence of more than 64 * words new tokens gets NaN rows */
+} fc_tree;
+
+/*
+ * tree_plan -- bits [tokens][words] and positions [tokens] of the trees that
+ * parents names: a node sees its ancestors and itself and sits its depth past
+ * kv_lens[b] - n.  Once a step, for all layers.  Of a sequence of more than 64 *
+ * words new tokens every bit is 0 and the position that of node 0.
+ */
+fc_status tree_plan(const int32_t *parents, const int32_t *cu_q, const int32_t *kv_lens, int32_t batch, int64_t tokens,
+                    int32_t words, uint64_t *bits, int32_t *positions, void *stream);
+
+/*
+ * chain_attn_tree -- chain_attn for trees: a node sees every slot before its
+ * sequence's first node (within the window, which counts positions) and the
+ * nodes of its bits; slopes and windows take the distance of positions, a slot
+ * before the tree being its own.  params->causal has to be set, the other
+ * arguments are chain_attn's.
+ */
+fc_status chain_attn_tree(const void *q, const int64_t *strides, const uint8_t *codes, const float *scales,
+                          const int32_t *table, const int32_t *cu_q, const int32_t *kv_lens, const fc_tree *tree,
+                          const float *slopes, const fc_attn_params *params, void *out, float *lse,
+                          const fc_kv_shape *shape, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * tree_accept -- walks each tree along the model's own choices: from node 0 on
+ * to the first child whose drafted token [tokens] is the token that targets
+ * [tokens] holds for the present node, until there is none.  keep
+ * [batch][max_keep]: the nodes passed, rising, then -1 (a path longer than
+ * max_keep ends there); kept [batch] their number; next [batch] = targets of the
+ * last one, the step's new token; lens [batch] = kv_lens - n + kept.  A sequence
+ * without new tokens has kept 0 and next -1.  Only nodes below node 0 can be
+ * kept.  lens may be kv_lens.
+ */
+fc_status tree_accept(const int32_t *parents, const int32_t *drafted, const int32_t *targets, const int32_t *cu_q,
+                      const int32_t *kv_lens, int32_t batch, int64_t tokens, int32_t max_keep, int32_t *keep,
+                      int32_t *kept, int32_t *next, int32_t *lens, void *stream);
+
+/*
+ * kv_keep -- of each sequence's n new tokens in the cache, those that keep
+ * [batch][max_keep] names (kept [batch] of them, rising, 0 .. n - 1) move to the
+ * slots kv_lens[b] - n + i, in all layers: codes [layers][pages]..., scales
+ * [layers][pages]....  A (page, head, side) that gets tokens takes the largest
+ * of its scale and of the pages' that they come from; where that is more than
+ * it had, its codes of earlier slots are rounded again, and a token that comes
+ * from a page of a smaller scale is rounded to it (nearest even).  Slots past
+ * the last kept one keep their bytes.  A sequence whose list is not as
+ * described stays as it is; a token whose own page is outside the pool is not
+ * moved, one that comes from such a page gets a NaN key and zero values.
+ * max_keep <= 64 * FC_TREE_WORDS; hq, dtype, max_q and max_kv of shape are
+ * checked and not used.  The pages written have to be their sequence's alone (kv_check with
+ * writes).
+ */
+fc_status kv_keep(uint8_t *codes, float *scales, int32_t layers, const int32_t *table, const int32_t *cu_q,
+                  const int32_t *kv_lens, const int32_t *keep, const int32_t *kept, int32_t max_keep,
+                  const fc_kv_shape *shape, void *stream);
+
+/*
+ * kv_copy -- page pairs[2 i] of the pool, codes and scales, to page pairs[2 i +
+ * 1], in all layers.  pairs is HOST memory, read before the call returns (a
+ * captured graph keeps the pairs of its capture).  FC_E_SHAPE, and nothing is
+ * copied, if an id is outside the pool, two pairs have one destination, or a
+ * destination is some pair's source; so the order of pairs does not matter.
+ * page and d as in fc_kv_shape.
+ */
+fc_status kv_copy(uint8_t *codes, float *scales, int32_t layers, int32_t pages, int32_t hkv, int32_t page, int32_t d,
+                  const int32_t *pairs, int64_t n, void *stream);
+
+/* How sample_tokens cuts a distribution: the arrays [rows] (device), or the one
+ * value for all rows where an array is NULL. */
+typedef struct {
+    const float *temperatures;
+    const int32_t *top_ks;
+    const float *top_ps;
+    const float *min_ps;
+    float temperature;      /* >= 0, finite; 0: the largest logit */
+    int32_t top_k;          /* >= 0; 0: off */
+    float top_p;            /* 0 .. 1; 1: off */
+    float min_p;            /* 0 .. 1; 0: off */
+} fc_sampling;
+
+/* Types of logits: those of fc_dtype and FC_F32. */
+enum { FC_F32 = 2 };
+
+/*
+ * sample_tokens -- out [rows] = a token drawn from each row of logits [rows,
+ * vocab] (row stride in elements, a row's logits adjacent) by the random number
+ * u [rows] in [0, 1).  Weights are w = exp((x - max) / temperature).  In the order of
+ * falling logits, equal ones by index, a token stays if
+ *   it is among the first top_k,
+ *   the weights before it are under top_p of what top_k left, and
+ *   its weight is at least min_p (of the largest one's, which is 1);
+ * the first one always stays.  The token drawn is the first, in order of index,
+ * at which the running sum of the weights that stay exceeds u times their sum.
+ * Temperatures <= 0 take the first token of that order.  Weights are computed in
+ * 64 bits and summed as integers in units of 2^-42, so that no order of sums
+ * changes a token; those under half a unit count as 0.  A logit of -inf is shut
+ * out; a row with a NaN or +inf, or with nothing else, gets -1, and so does a
+ * row with u NaN.  From arrays: top_k < 0 and top_p >= 1 are off, values under
+ * 0 or over 1 are taken to the nearer end, a temperature that is NaN is as 0; a
+ * u outside [0, 1) is taken to its end.  vocab <= 2^20.  workspace: device
+ * memory of sample_workspace's size, 16-byte aligned, not shared by calls that
+ * may run at once.
+ */
+fc_status sample_tokens(const void *logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t stride, const float *u,
+                        const fc_sampling *sampling, int32_t *out, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+/* Bytes of workspace that sample_tokens needs for these sizes (host only). */
+fc_status sample_workspace(int32_t dtype, int64_t rows, int32_t vocab, int64_t *bytes);
+
 /*
  * kv_check -- looks HOST copies of a batch's metadata over: cu_q starts at 0,
  * does not fall and ends within tokens; every length is within its sequence's
