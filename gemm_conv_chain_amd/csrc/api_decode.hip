@@ -15,7 +15,8 @@ hipError_t run_kv_copy(uint8_t* codes, float* scales, int layers, int pages, int
                        hipStream_t st);
 hipError_t run_sample(int dtype, const void* logits, long rows, int vocab, long stride, const float* u, const float* temperatures,
                       const int* top_ks, const float* top_ps, const float* min_ps, float temperature, int top_k, float top_p,
-                      float min_p, int* out, hipStream_t st);
+                      float min_p, int* out, void* workspace, hipStream_t st);
+long sample_space(long rows, int vocab);
 }  // namespace fc
 
 namespace {
@@ -124,7 +125,7 @@ fc_status sample_workspace(int32_t dtype, int64_t rows, int32_t vocab, int64_t* 
     fc_status s = check_logits(dtype, rows, vocab);
     if (s != FC_OK) return s;
     if (!bytes) return fail(FC_E_NULL, "bytes is NULL");
-    *bytes = 0;
+    *bytes = fc::sample_space(rows, vocab);
     return done(hipSuccess, "");
 }
 
@@ -147,10 +148,13 @@ fc_status sample_tokens(const void* logits, int32_t dtype, int64_t rows, int32_t
     if (!aligned(u, 4) || !aligned(out, 4) || !aligned(g.temperatures, 4) || !aligned(g.top_ks, 4) || !aligned(g.top_ps, 4) ||
         !aligned(g.min_ps, 4))
         return fail(FC_E_ALIGN, "u, out and the settings' arrays must be 4-byte aligned");
-    (void)workspace;
-    (void)workspace_bytes;
+    const int64_t need = fc::sample_space(rows, vocab);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(workspace ? FC_E_SHAPE : FC_E_NULL, "a workspace of %lld bytes is required, got %lld", (long long)need,
+                    (long long)workspace_bytes);
+    if (!aligned(workspace, 16)) return fail(FC_E_ALIGN, "workspace must be 16-byte aligned");
     return done(fc::run_sample(dtype, logits, rows, vocab, stride, u, g.temperatures, g.top_ks, g.top_ps, g.min_ps,
-                               g.temperature, g.top_k, g.top_p, g.min_p, out, (hipStream_t)stream),
+                               g.temperature, g.top_k, g.top_p, g.min_p, out, workspace, (hipStream_t)stream),
                 "sample_tokens");
 }
 
