@@ -360,39 +360,40 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         return x > cut_x || (x == cut_x && i <= cut_i);
     }
 
-    // f(index, logit, weight()) for lo .. hi - 1 (lo a multiple of 8), by `threads` of which this is
-    // number t; -inf for what is none of them.  Four logits' work together: more take more registers
-    // than there are.
-    template <class F> __device__ __forceinline__ void each(int lo, int hi, int t, int threads, F&& f) const
+    // f(index, logit, weight()) for lo .. hi - 1, by one wave: lo and, but for the row's end, hi are
+    // multiples of 512. -inf for what is past the row's end. Four logits' work together: more take more
+    // registers than there are.
+    template <class F> __device__ __forceinline__ void each(int lo, int hi, F&& f) const
     {
         constexpr int U = 2;   // loads of this step, and as many of the next on the way
-        const int step = threads * 8;
         Eight<L> next[U];
 #pragma unroll
-        for (int k = 0; k < U; ++k) next[k] = fetch(row, lo + t * 8 + k * step, a.vocab);
+        for (int k = 0; k < U; ++k) next[k] = fetch(row, lo + lane * 8 + k * 512, a.vocab);
 #pragma unroll 1
-        for (int base = lo; base < hi; base += step * U) {
-            const bool whole = base + step * U <= hi;   // (else what is past hi is left out, too)
+        for (int base = lo; base < hi; base += 512 * U) {
             Eight<L> e[U];
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 e[k] = next[k];
-                next[k] = fetch(row, base + step * (U + k) + t * 8, a.vocab);
+                next[k] = fetch(row, base + 512 * (U + k) + lane * 8, a.vocab);
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int k = 0; k < U; ++k) {
+                const int b = base + k * 512;
+                if (b >= hi) break;
                 float x[8];
-                const int at = unpack(e[k], base + t * 8 + k * step, a.vocab, whole, x);
+                const int at = unpack(e[k], b + lane * 8, a.vocab, b + 512 <= a.vocab, x);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float y = whole || at + j < hi ? x[j] : kNegInf;
+                    const float y = x[j];
                     f(at + j, y, [&] { return weight(y); });
                     if (j % 4 == 3) __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
     }
+
     // The same as sources of elements: all of the row (a wave has a sixteenth of it), n elements of
     // s.list, n groups' largest (as weights 1).
     __device__ __forceinline__ int part() const { return ((a.vocab + WAVES - 1) / WAVES + 511) / 512 * 512; }
@@ -401,7 +402,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         template <class F> __device__ __forceinline__ void operator()(F&& f) const
         {
             const int per = p.part(), lo = p.wave * per, hi = lo + per < p.a.vocab ? lo + per : p.a.vocab;
-            p.each(lo, hi, p.lane, 64, f);
+            p.each(lo, hi, f);
         }
     };
     struct Listed {
@@ -530,7 +531,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             const int per = ((hi - lo + WAVES - 1) / WAVES + 511) / 512 * 512;
             const int z = lo + (wave + 1) * per < hi ? lo + (wave + 1) * per : hi;
             u64 sum = 0;
-            if (!known) each(lo + wave * per, z, lane, 64, [&](int i, float x, auto&& weight) { sum += w(i, x, weight); });
+            if (!known) each(lo + wave * per, z, [&](int i, float x, auto&& weight) { sum += w(i, x, weight); });
             sum = known ? mine : wave_sum(sum);
             known = false;
             if (lane == 0) s.wave_mass[wave] = sum;
@@ -551,16 +552,17 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         return locate_here<1>(lo, hi, goal, [&](int i, float x) { return w(i, x, [&] { return weight(x); }); });
     }
 
-    // A histogram of which(x) over the source's elements, of their weights or (by_mass false) number.
-    // The last bin's, which may be most of them, are added up in registers.
-    template <class S, class B> __device__ __forceinline__ void fill_bins(const S& source, bool by_mass, B&& which)
+    // A histogram of which(x) over the source's elements, of their weights or (MASS false) number.
+    // The last bin's, which may be most of them (-inf among them, as nothing), are added up in registers.
+    template <bool MASS, class S, class B> __device__ __forceinline__ void fill_bins(const S& source, B&& which)
     {
         clear_bins();
         u64 rest = 0;
         source([&](int, float x, auto&& weight) {
             const int b = which(x);
             if (b < 0) return;
-            const u64 v = by_mass ? weight() : 1;
+            u64 v = x > kNegInf;
+            if constexpr (MASS) v = weight();
             if (b == BINS - 1) rest += v;
             else add_bin(b, v);
         });
@@ -568,14 +570,14 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         if (lane == 0 && rest) add_bin(BINS - 1, rest);
     }
 
-    // The last element that stays, in s.cut_x and s.cut_i: the goal-th in falling order, or (by_mass)
+    // The last element that stays, in s.cut_x and s.cut_i: the goal-th in falling order, or (MASS)
     // that at which the mass reaches goal; `share` > 0: that share of the whole mass.  False where there are not so many.  `tie(many, x)`: the
     // index of the many-th element that is x.  Of a row, *mine: the sum of this wave's part in the bins
     // before the cut's, whose largest value may be s.cut_top.
-    template <class S, class T> __device__ __forceinline__ bool cut_at(const S& source, bool by_mass, u64 goal, float share, T&& tie,
-                                           u64* mine)
+    template <bool MASS, class S, class T>
+    __device__ __forceinline__ bool cut_at(const S& source, u64 goal, float share, T&& tie, u64* mine)
     {
-        fill_bins(source, by_mass, [&](float x) { return x > kNegInf ? bin(x) : -1; });
+        fill_bins<MASS>(source, [&](float x) { return bin(x); });
         if (ROW && share > 0.0f) {
             __syncthreads();
             u64 v = 0;
@@ -607,7 +609,11 @@ template <class L, int WAVES, bool ROW> struct Sampler {
                 unsigned at = 0;
                 if (lane == first) at = lds_add(&s.n_few, (unsigned)__builtin_popcountll(here));
                 at = __builtin_amdgcn_readlane(at, first) + __builtin_popcountll(here & ((1ull << lane) - 1));
-                if (at < SR_FEW) s.few[at] = entry(x, i, by_mass ? weight() : 1);
+                if (at < SR_FEW) {
+                    u64 w = 1;
+                    if constexpr (MASS) w = weight();
+                    s.few[at] = entry(x, i, w);
+                }
             });
             if (most) {
                 lds_min(&s.key_lo, least);
@@ -635,7 +641,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             hi = s.key_hi;
             if (lo == hi) {       // all equal: the first few by index
                 const float x = from_key(lo);
-                const u64 w = by_mass ? weight(x) : 1;
+                const u64 w = MASS ? weight(x) : 1;
                 const int index = tie((goal + w - 1) / w, x);
                 if (tid == 0) {
                     s.cut_x = x;
@@ -647,7 +653,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             int shift = 0;
             while ((hi - lo) >> shift >= BINS) ++shift;
             const float ya = from_key(lo), yb = from_key(hi);
-            fill_bins(source, by_mass, [&](float x) { return x >= ya && x <= yb ? (int)((hi - order_key(x)) >> shift) : -1; });
+            fill_bins<MASS>(source, [&](float x) { return x >= ya && x <= yb ? (int)((hi - order_key(x)) >> shift) : -1; });
             const int sub = find_bin(goal, &ahead);
             goal -= ahead;
             const unsigned top = hi - ((unsigned)sub << shift);   // the largest key of the sub-bin
@@ -705,19 +711,23 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         int cut_i = 0x7fffffff;
         const Whole source{*this};
         u64 mine = 0;
-#pragma unroll 1
-        for (int by_mass = 0; by_mass < 2; ++by_mass) {   // (one copy of cut_at)
-            if (by_mass ? !(set.p < 1.0f) : set.k == 0) continue;
-            u64 goal = set.k;
-            if (by_mass && set.k > 0) {   // of what top_k left
-                u64 left = 0;
-                source([&](int i, float x, auto&& weight) { left += stays(x, i, cut_x, cut_i) ? weight() : 0; });
-                goal = (u64)__builtin_ceil((double)set.p * (double)block_sum(left));
+        const auto tie = [&](u64 many, float x) {
+            return locate(many - 1, false, 0.0f, false, 0, [&](int, float y, auto&&) { return y == x ? 1ull : 0ull; });
+        };
+        if (set.k > 0) {
+            if (cut_at<false>(source, set.k, 0.0f, tie, &mine)) {
+                cut_x = s.cut_x;
+                cut_i = s.cut_i;
             }
-            const auto tie = [&](u64 many, float x) {
-                return locate(many - 1, false, 0.0f, false, 0, [&](int, float y, auto&&) { return y == x ? 1ull : 0ull; });
-            };
-            if (cut_at(source, by_mass, goal, by_mass && set.k == 0 ? set.p : 0.0f, tie, &mine)) {
+            __syncthreads();
+        }
+        if (set.p < 1.0f) {
+            u64 left = 0;   // of what top_k left, or of the whole
+            if (set.k > 0) {
+                source([&](int i, float x, auto&& weight) { left += stays(x, i, cut_x, cut_i) ? weight() : 0; });
+                left = (u64)__builtin_ceil((double)set.p * (double)block_sum(left));
+            }
+            if (cut_at<true>(source, left, set.k > 0 ? 0.0f : set.p, tie, &mine)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             }
@@ -750,18 +760,22 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         const Entry e = tid < n ? s.list[tid] : Entry{0, 0, 0, 0};
         const float x = __builtin_bit_cast(float, (unsigned)e[0]);
         u64 w = tid < n ? high_pair(e) : 0;
-#pragma unroll 1
-        for (int by_mass = 0; by_mass < 2; ++by_mass) {
-            if (by_mass ? !(set.p < 1.0f) : set.k == 0) continue;
-            if (by_mass && set.k > 0) all = block_sum(stays(x, e[1], cut_x, cut_i) ? w : 0);
-            const u64 goal = by_mass ? (u64)__builtin_ceil((double)set.p * (double)all) : set.k;
-            const auto tie = [&](u64 many, float y) {
-                return index_at(many - 1, n, [&](int, float z, u64) { return z == y ? 1ull : 0ull; });
-            };
-            if (cut_at(source, by_mass, goal, 0.0f, tie, nullptr)) {
+        const auto tie = [&](u64 many, float y) {
+            return index_at(many - 1, n, [&](int, float z, u64) { return z == y ? 1ull : 0ull; });
+        };
+        if (set.k > 0) {
+            if (cut_at<false>(source, set.k, 0.0f, tie, nullptr)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
-            } else if (by_mass && !floored) {
+            }
+            __syncthreads();
+        }
+        if (set.p < 1.0f) {
+            if (set.k > 0) all = block_sum(stays(x, e[1], cut_x, cut_i) ? w : 0);
+            if (cut_at<true>(source, (u64)__builtin_ceil((double)set.p * (double)all), 0.0f, tie, nullptr)) {
+                cut_x = s.cut_x;
+                cut_i = s.cut_i;
+            } else if (!floored) {
                 return SR_NOT_YET;
             }
             __syncthreads();
@@ -785,9 +799,9 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         if (first <= (unsigned)ngroups) {
             const Tops<G> source{*this, groups, ngroups};
             if (again) {
-                if (cut_at(source, false, first, 0.0f, [](u64, float) { return 0; }, nullptr)) floor = s.cut_x;
+                if (cut_at<false>(source, first, 0.0f, [](u64, float) { return 0; }, nullptr)) floor = s.cut_x;
             } else {
-                fill_bins(source, false, [&](float x) { return x > kNegInf ? bin(x) : -1; });
+                fill_bins<false>(source, [&](float x) { return bin(x); });
                 u64 ahead;
                 const int b = find_bin(first, &ahead);
                 if (b >= 0) floor = from_key(edge(b));
