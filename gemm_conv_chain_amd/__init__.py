@@ -209,6 +209,7 @@ def _load(path):
     L.kv_check.argtypes = [_vp, _vp, _vp, ctypes.POINTER(KvShape), _i32]
     L.chain_attn_tree.argtypes = [_vp, ctypes.POINTER(_i64), _vp, _vp, _vp, _vp, _vp, ctypes.POINTER(Tree), _vp,
                                   ctypes.POINTER(AttnParams), _vp, _vp, ctypes.POINTER(KvShape), _vp, _i64, _vp]
+    L.chain_attn_tree_plan.argtypes = L.chain_attn_plan.argtypes
     L.tree_plan.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp]
     L.tree_accept.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _i64, _i32, _vp, _vp, _vp, _vp, _vp]
     L.kv_keep.argtypes = [_vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, ctypes.POINTER(KvShape), _vp]
@@ -217,7 +218,7 @@ def _load(path):
     L.sample_tokens.argtypes = [_vp, _i32, _i64, _i32, _i64, _vp, ctypes.POINTER(Sampling), _vp, _vp, _i64, _vp]
     L.fc_tune_clear.restype = None
     L.fc_tune_clear.argtypes = []
-    for name in ("chain_attn_tree", "tree_plan", "tree_accept", "kv_keep", "kv_copy", "sample_workspace", "sample_tokens",
+    for name in ("chain_attn_tree", "chain_attn_tree_plan", "tree_plan", "tree_accept", "kv_keep", "kv_copy", "sample_workspace", "sample_tokens",
                  "rope_apply", "kv_append", "chain_attn_plan", "chain_attn", "kv_check", "chain_conv2_auto_config", "chain_conv2_ex", "chain_conv2_variant", "chain_conv2_tune", "winograd_weights", "chain_conv_pool_winograd", "chain_gemm2_ex", "chain_gemm2_tune_ex", "chain_gemm2_auto_config", "chain_conv_pool_tune",
                  "chain_conv_pool_auto_config", "chain_conv_pool_ex", "avgpool2x2", "fc_probe_mfma", "fc_probe_read", "chain_conv_bn_pool", "chain_convN", "chain_convN_variant", "chain_convN_auto_variant", "chain_convN_tune", "chain_gemm2_tune", "chain_gemm2_auto_variant", "chain_gemm2", "chain_gemm2_variant", "chain_gemmN", "chain_conv_pool", "chain_conv2", "gemm_bias_act",
                  "conv_bias_act", "maxpool2x2", "pad_channels"):
@@ -1074,12 +1075,14 @@ _ATTN_VARIANT_NAME = {v: k for k, v in ATTN_VARIANT.items()}
 
 
 def attn_plan(tokens, batch, hq, hkv, d, page, table_stride, max_q, max_kv, dtype="bfloat16", causal=True, window=0,
-              variant="auto", splits=0):
+              variant="auto", splits=0, tree=False):
     """{variant, splits, chunk, workspace}: the kernel form chain_attn runs, the blocks
-    a sequence's keys are split over, keys a block, workspace bytes (host only)."""
+    a sequence's keys are split over, keys a block, workspace bytes (host only);
+    ``tree``: of a call with a tree."""
     sh = KvShape(DTYPE[dtype], batch, hq, hkv, d, page, 1, table_stride, tokens, max_q, max_kv)
     plan = AttnPlan()
-    _check("chain_attn_plan", lib().chain_attn_plan(sh, _attn_params(d, None, causal, 0.0, window, variant, splits), plan))
+    f = lib().chain_attn_tree_plan if tree else lib().chain_attn_plan
+    _check("chain_attn_plan", f(sh, _attn_params(d, None, causal, 0.0, window, variant, splits), plan))
     return {"variant": _ATTN_VARIANT_NAME[plan.variant], "splits": int(plan.splits), "chunk": int(plan.chunk),
             "workspace": int(plan.workspace)}
 
@@ -1135,7 +1138,7 @@ def chain_attn(q, codes, scales, table, cu_q, kv_lens, scale=None, causal=True, 
     _one_device(dev, (codes, scales, table, cu_q, kv_lens, slopes, out, le, workspace, bits, positions))
     L = lib()
     plan = AttnPlan()
-    s = L.chain_attn_plan(sh, pa, plan)
+    s = (L.chain_attn_plan if tr is None else L.chain_attn_tree_plan)(sh, pa, plan)
     if s:
         _check("chain_attn", s)
     if out is None:

@@ -208,6 +208,47 @@ void plan_attn(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
     out->workspace = n > 1 ? s->tokens * s->hq * n * (s->d + 4) * 4 : 0;
 }
 
+// The tile form's part in a tree call: `even` blocks for each head and row tile among which the
+// stages of all sequences are shared (0: a block a tile), and slots for the parts of sequences that
+// several of them have.
+struct TreeTiles {
+    int64_t even, row_tiles, slots, rows;
+};
+
+// As many blocks as the machine holds at once, two a CU for heads of 64 and 128 and one for larger
+// ones (registers and shared memory), with no less than eight stages each.  More tiles than four
+// times that need no sharing.  (The prefix sums over sequences in each block are for thousands of
+// these at most.)
+TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
+{
+    const int64_t G = s->hq / s->hkv, rows = s->d <= 128 ? 128 : 256, keys = s->d <= 192 ? 64 : 32;
+    const int64_t room = (int64_t)fc::device_cu_count() * (s->d <= 128 ? 2 : 1);
+    TreeTiles t;
+    t.rows = rows;
+    t.row_tiles = ((s->max_q > 0 ? s->max_q : 1) * G + rows - 1) / rows;
+    const int64_t heads = t.row_tiles * s->hkv;
+    const int64_t stages = s->batch * (key_blocks(s, p, 0x7fffffff) * 16 / keys + 1);
+    t.even = p->splits > 0 ? (int64_t)p->splits * s->batch : (room + heads / 2) / heads;
+    if (p->splits == 0) {
+        t.even = t.even < stages / 8 ? t.even : stages / 8;
+        if (s->batch * heads >= 4 * room || t.even <= 1) t.even = 0;
+    }
+    if (s->batch > 4096 || p->splits == 1 || t.even * t.row_tiles > 0x7fffffff / 256 || heads > 65535) t.even = 0;
+    t.slots = t.even ? t.even + s->batch : 0;
+    return t;
+}
+
+void plan_tree(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
+{
+    plan_attn(s, p, out);
+    if (out->variant != FC_ATTN_TILE) return;
+    const TreeTiles t = tree_tiles(s, p);
+    const int64_t batch = s->batch > 0 ? s->batch : 1, per = t.even ? (t.even + batch - 1) / batch : 1;
+    out->splits = (int32_t)per;
+    out->chunk = (int32_t)((key_blocks(s, p, 0x7fffffff) + per - 1) / per * 16);
+    out->workspace = t.even ? t.slots * t.row_tiles * t.rows * s->hkv * (s->d + 4) * 4 + s->batch * 8 : 0;
+}
+
 // A tree's words and pairing with the scores' order; its pointers are looked at with the others.
 fc_status check_tree(const fc_tree* t, const fc_attn_params* p)
 {
@@ -236,11 +277,12 @@ fc_status attn_call(const void* q, const int64_t* strides, const uint8_t* codes,
         return fail(FC_E_ALIGN, "q, out and workspace must be 16-byte, lse and slopes 4-byte aligned");
     if ((s = check_cache(shape, codes, scales, table, cu_q, kv_lens)) != FC_OK) return s;
     fc_attn_plan p;
-    plan_attn(shape, params, &p);
+    if (tree) plan_tree(shape, params, &p);
+    else plan_attn(shape, params, &p);
     if (p.workspace > 0 && (!workspace || workspace_bytes < p.workspace))
         return fail(workspace ? FC_E_SHAPE : FC_E_NULL, "a workspace of %lld bytes is required, got %lld",
                     (long long)p.workspace, (long long)workspace_bytes);
-    fc::AttnArgs a;
+    fc::AttnArgs a{};
     a.q = q;
     a.q_ts = strides[0];
     a.q_hs = strides[1];
@@ -268,8 +310,17 @@ fc_status attn_call(const void* q, const int64_t* strides, const uint8_t* codes,
     a.tree_pos = tree ? tree->positions : nullptr;
     a.tree_words = tree ? tree->words : 0;
     const bool tile = p.variant == FC_ATTN_TILE;
-    hipError_t e = tree ? (tile ? fc::run_attn_tile_tree(shape->dtype, a, (hipStream_t)stream)
-                                : fc::run_attn_rows_tree(shape->dtype, a, (hipStream_t)stream))
+    if (tree && tile) {
+        const TreeTiles t = tree_tiles(shape, params);
+        a.even = (int)t.even;
+        a.slots = (int)t.slots;
+        const int64_t part_rows = t.slots * t.row_tiles * t.rows * shape->hkv;
+        a.part_ml = t.even ? (fc::floatx4*)(a.part_o + part_rows * shape->d) : nullptr;
+        a.ends = t.even ? (int*)(a.part_ml + part_rows) : nullptr;
+        a.nsplit = 1;
+        return done(fc::run_attn_tile_tree(shape->dtype, a, (hipStream_t)stream), "chain_attn_tree");
+    }
+    hipError_t e = tree ? fc::run_attn_rows_tree(shape->dtype, a, (hipStream_t)stream)
                         : (tile ? fc::run_attn_tile(shape->dtype, a, (hipStream_t)stream)
                                 : fc::run_attn_rows(shape->dtype, a, (hipStream_t)stream));
     if (e == hipSuccess && p.splits > 1) e = fc::run_attn_join(shape->dtype, a, (hipStream_t)stream);
@@ -328,6 +379,17 @@ fc_status chain_attn_plan(const fc_kv_shape* shape, const fc_attn_params* params
     if ((s = check_params(shape, params)) != FC_OK) return s;
     if (!plan) return fail(FC_E_NULL, "plan is NULL");
     plan_attn(shape, params, plan);
+    return done(hipSuccess, "");
+}
+
+fc_status chain_attn_tree_plan(const fc_kv_shape* shape, const fc_attn_params* params, fc_attn_plan* plan)
+{
+    fc_status s = check_shape(shape);
+    if (s != FC_OK) return s;
+    if ((s = check_params(shape, params)) != FC_OK) return s;
+    if (!params->causal) return fail(FC_E_ARG, "a tree needs causal scores");
+    if (!plan) return fail(FC_E_NULL, "plan is NULL");
+    plan_tree(shape, params, plan);
     return done(hipSuccess, "");
 }
 

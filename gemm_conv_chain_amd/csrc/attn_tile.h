@@ -45,7 +45,32 @@ typedef FC_LDS uint8_t lds_u8;
 __host__ __device__ constexpr int tile_waves(int d) { return d <= 128 ? 4 : 8; }
 __host__ __device__ constexpr int tile_blocks(int d) { return d <= 192 ? 4 : 2; }
 
-// TREE: see k_attn_rows.
+// The stages of KB blocks of keys that a sequence's rows see, at least one (so that its rows are
+// written), and none without new tokens.
+template <int KB> __device__ __forceinline__ int tree_stages(const AttnArgs& a, int b)
+{
+    long tok0;
+    int nq, lo, hi;
+    bool over;
+    seq_range(a.cu_q, a.s, b, &tok0, &nq);
+    int kv_len = seq_keys(a.kv_lens, a.s, b, &over);
+    if (nq > 64 * a.tree_words) kv_len = 0;
+    key_range(a, kv_len, kv_len - nq, 0, nq - 1, &lo, &hi);
+    return nq == 0 ? 0 : hi - lo > KB ? (hi - lo + KB - 1) / KB : 1;
+}
+
+// A value that all lanes have alike, kept where that is known (scalar registers).
+__device__ __forceinline__ int alike(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ long alike(long v)
+{
+    return (long)((unsigned long)(unsigned)alike((int)(v >> 32)) << 32 | (unsigned)alike((int)v));
+}
+
+// TREE: see k_attn_rows.  A step's trees have few tiles and lengths of all sizes; with
+// the keys of each in as many parts, the longest sequence's blocks end last.  So the
+// stages of all sequences are dealt out evenly to as many blocks as the machine
+// holds at once (AttnArgs::even); the tiles of a sequence go through the same keys
+// side by side, so that these are read from memory once.
 template <class T, int D, int NW, int MODE, bool TREE>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_tiles)
 {
@@ -83,7 +108,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
     const int v_to = SIDE + ((blk >> 1) * 4 + (blk & 1)) * (16 * D) + lane * 16;
     const int k_at = hf * 1024 + (n ^ (4 * hf)) * 16, v_at = SIDE + hf * (16 * D) + n * 16;
 
-    for (int b = blockIdx.z; b < s.batch; b += gridDim.z) {
+    // Tile of rows from r0 on of sequence b; TREE: the stages first .. last - 1 of its keys, slot < 0 if
+    // these are all.
+    auto tile = [&](int b, int r0, int first, int last, int slot) __attribute__((always_inline)) {
         long tok0;
         int nq;
         seq_range(a.cu_q, s, b, &tok0, &nq);
@@ -98,7 +125,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
         const int* const row_of = a.table + (size_t)b * s.table_stride;
         const uint8_t* const head = a.codes + side_base(0, h, 0, s);
         const size_t page_bytes = (size_t)s.hkv * 2 * s.page * D;
-        for (int r0 = rt0 * BR; r0 < rows; r0 += row_tiles * BR) {
+        {
             const int r1 = r0 + BR < rows ? r0 + BR : rows;
             int g_lo, g_hi;
             key_range(a, kv_len, pos0, TREE ? 0 : a.by_g.div(r0), TREE ? nq - 1 : a.by_g.div(r1 - 1), &g_lo, &g_hi);
@@ -130,8 +157,9 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
             float m = kNegInf, mb = 0.0f;   // what weights refer to, a maximum less UP; with 0 for -inf
             float l = 0.0f, le = 0.0f;      // sums of rounded and (for lse) of exact weights
 
-            for (int c0 = g_lo + split * a.chunk; c0 < g_hi; c0 += a.nsplit * a.chunk) {
-                const int c1 = c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
+            const int c_end = TREE && last < (g_hi - g_lo + KB - 1) / KB ? g_lo + last * KB : g_hi;
+            for (int c0 = g_lo + (TREE ? first * KB : split * a.chunk); c0 < c_end; c0 = TREE ? c_end : c0 + a.nsplit * a.chunk) {
+                const int c1 = TREE ? c_end : c0 + a.chunk < g_hi ? c0 + a.chunk : g_hi;
                 // Loads of this wave's share of the stage at block k0, the page's id already here.
                 auto block_of = [&](int k0) { return k0 + blk < c1 ? k0 + blk : c1 - 1; };
                 auto load_id = [&](int k0) {
@@ -357,7 +385,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
             le = over ? l : sum_x32(le);
             if (r < rows) {
                 const long row = (tok0 + t) * s.hq + hq;
-                if (a.nsplit == 1) {
+                if (TREE ? slot < 0 : a.nsplit == 1) {
                     const float inv = l != 0.0f ? 1.0f / l : 0.0f;   // no key seen: 0
                     T* out = (T*)a.out + row * D + 4 * hf;
 #pragma unroll
@@ -371,7 +399,7 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                         }
                     if (a.lse && hf == 0) a.lse[row] = (m * unit + __builtin_amdgcn_logf(le)) * (1.0f / kLog2e);
                 } else {
-                    const long at = row * a.nsplit + split;
+                    const long at = TREE ? ((long)h * row_tiles * a.slots + slot) * BR + (r - r0) : row * a.nsplit + split;
                     if (l != 0.0f) {
                         float* out = a.part_o + at * D + 4 * hf;
 #pragma unroll
@@ -385,6 +413,82 @@ __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_ti
                 }
             }
         }
+    };
+    if constexpr (!TREE) {
+        for (int b = blockIdx.z; b < s.batch; b += gridDim.z) {
+            long tok0;
+            int nq;
+            seq_range(a.cu_q, s, b, &tok0, &nq);
+            for (int r0 = rt0 * BR; r0 < nq * a.G; r0 += row_tiles * BR) tile(b, r0, 0, 0, 0);
+        }
+    } else {
+        // This block's part of the stages: z of a.even; from stage `first` of sequence b on, `left` of them.
+        int b = (int)blockIdx.z, z = 0, first = 0, stages = 0;
+        long left = 0;
+        const int rt_first = blockIdx.y % row_tiles;
+        if (a.even) {
+            long total = 0;
+            for (int b0 = 0; b0 < s.batch; b0 += 64) {
+                long w = b0 + lane < s.batch ? tree_stages<KB>(a, b0 + lane) : 0;
+#pragma unroll
+                for (int k = 32; k; k >>= 1) w += __shfl_xor(w, k);
+                total += w;
+            }
+            total = alike(total);
+            const long parts = a.even < total ? a.even : total;
+            z = blockIdx.y / row_tiles;
+            if (z >= parts) return;
+            const long pos = z * total / parts;
+            left = (z + 1) * total / parts - pos;
+            long before = 0;
+            for (int b0 = 0;; b0 += 64) {   // (pos < total: some sequence has it)
+                const int w = b0 + lane < s.batch ? tree_stages<KB>(a, b0 + lane) : 0;
+                long upto = w;
+#pragma unroll
+                for (int k = 1; k < 64; k <<= 1) {
+                    const long o = __shfl_up(upto, k);
+                    upto += lane >= k ? o : 0;
+                }
+                const unsigned long long past = __ballot(before + upto > pos);
+                if (past) {
+                    const int at = __builtin_ctzll(past);
+                    b = b0 + at;
+                    stages = __builtin_amdgcn_readlane(w, at);
+                    first = alike((int)(pos - before - __shfl(upto - w, at)));
+                    break;
+                }
+                before = alike(before + __shfl(upto, 63));
+            }
+        }
+        while (b < s.batch) {
+            const int last = !a.even ? 0x7fffffff : left < stages - first ? first + (int)left : stages;
+            const bool begins = first == 0, ends = !a.even || last == stages;
+            if (a.even && h == 0 && rt_first == 0 && threadIdx.x == 0) {
+                if (begins) a.ends[2 * b] = z;
+                if (ends) a.ends[2 * b + 1] = z;
+            }
+            long tok0;
+            int nq;
+            seq_range(a.cu_q, s, b, &tok0, &nq);
+            // (tiles past those that max_q promised are whole, the first block's)
+            for (int rt = rt_first; rt * BR < nq * a.G; rt += row_tiles) {
+                const bool shared = rt < row_tiles && !(begins && ends);
+                if (rt >= row_tiles && !begins) break;
+                const bool whole = !shared;
+                tile(b, rt * BR, whole ? 0 : first, whole ? 0x7fffffff : last, whole ? -1 : rt * a.slots + z + b);
+            }
+            if (!a.even) {
+                b += gridDim.z;
+                continue;
+            }
+            left -= last - first;
+            if (left <= 0) break;
+            first = 0;
+            do {
+                ++b;
+                stages = alike(tree_stages<KB>(a, b));
+            } while (stages == 0);
+        }
     }
 }
 
@@ -397,6 +501,11 @@ static hipError_t launch_tile(const AttnArgs& a, hipStream_t st)
     if (e != hipSuccess) return e;
     const long rows = (long)(a.s.max_q > 0 ? a.s.max_q : 1) * a.G;
     long rt = (rows + 32 * NW - 1) / (32 * NW);
+    if (TREE && a.even) {
+        const int lds = 2 * 2 * 16 * tile_blocks(D) * D * 2;
+        k_attn_tile<T, D, NW, MODE, TREE><<<dim3(a.s.hkv, (unsigned)(rt * a.even)), dim3(64 * NW), lds, st>>>(a, (int)rt);
+        return hipGetLastError();
+    }
     if (rt * a.nsplit > 65535) rt = 65535 / a.nsplit;
     // heads fastest: workgroups go round-robin over the 8 XCDs, so that the row
     // tiles of a head, which read the same codes, meet in one L2 (hkv % 8 == 0)
@@ -421,6 +530,101 @@ static hipError_t tile_by_d(const AttnArgs& a, hipStream_t st)
     case 192: return tile_mode<T, 192, TREE>(a, st);
     default: return tile_mode<T, 256, TREE>(a, st);
     }
+}
+
+// Joins the parts of a sequence that several blocks had, as k_attn_join does for splits: a wave four
+// rows side by side, as one alone is a chain of loads (32 trees of 26 nodes in two or three parts: 22
+// us). The weights of up to 64 parts wait in the lanes, so that the parts are asked for at once.
+template <class T, int D>
+__global__ __launch_bounds__(256) void k_attn_tree_join(AttnArgs a, int row_tiles)
+{
+    constexpr int N = D <= 128 ? 4 : 2, BR = 32 * tile_waves(D);
+    const int b = blockIdx.x, h = blockIdx.y / row_tiles, rt = blockIdx.y % row_tiles, lane = threadIdx.x & 63;
+    const int rr = blockIdx.z * 4 * N + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * N;
+    long tok0;
+    int nq;
+    seq_range(a.cu_q, a.s, b, &tok0, &nq);
+    const int rows = nq * a.G - rt * BR - rr;   // from rr on
+    const int z0 = a.ends[2 * b], n = a.ends[2 * b + 1] - z0 + 1;
+    if (rows <= 0 || n <= 1) return;
+    const long at = ((long)blockIdx.y * a.slots + z0 + b) * BR + rr;
+    const floatx4* ml = a.part_ml + at;
+    float ms[N], m[N], l[N], le[N], o[N][4];
+#pragma unroll
+    for (int i = 0; i < N; ++i) m[i] = kNegInf;
+    for (int k = lane; k < n; k += 64)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            m[i] = fmaxf(m[i], ml[(long)k * BR + (i < rows ? i : 0)][0]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        m[i] = max_x32(max_x16(m[i]));
+#pragma unroll
+        for (int k = 8; k; k >>= 1) m[i] = fmaxf(m[i], __shfl_xor(m[i], k));
+        ms[i] = m[i] == kNegInf ? 0.0f : m[i];
+        l[i] = le[i] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][e] = 0.0f;
+    }
+    const float* p = a.part_o + at * D + lane;
+    for (int k0 = 0; k0 < n; k0 += 64) {
+        float f[N];
+        int some[N];   // (a part that saw no key has not written its o)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const floatx4 v = ml[(long)(k0 + lane < n ? k0 + lane : 0) * BR + (i < rows ? i : 0)];
+            some[i] = v[1] != 0.0f && k0 + lane < n;
+            f[i] = some[i] ? __builtin_amdgcn_exp2f(v[0] - ms[i]) : 0.0f;
+            l[i] += some[i] ? v[1] * f[i] : 0.0f;
+            le[i] += some[i] ? v[2] * f[i] : 0.0f;
+        }
+        const int many = n - k0 < 64 ? n - k0 : 64;
+#pragma unroll 4
+        for (int k = 0; k < many; ++k) {
+            float y[N][4];
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) y[i][e] = p[((long)(k0 + k) * BR + (i < rows ? i : 0)) * D + e * 64];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f[i]), k));
+                const bool has = __builtin_amdgcn_readlane(some[i], k) != 0;
+#pragma unroll
+                for (int e = 0; e < D / 64; ++e) o[i][e] += has ? y[i][e] * w : 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (i >= rows) break;
+#pragma unroll
+        for (int k = 32; k; k >>= 1) {
+            l[i] += __shfl_xor(l[i], k);
+            le[i] += __shfl_xor(le[i], k);
+        }
+        const int r = rt * BR + rr + i, t = a.by_g.div(r), hq = h * a.G + (r - t * a.G);
+        const long row = (tok0 + t) * a.s.hq + hq;
+        const float inv = l[i] != 0.0f ? 1.0f / l[i] : 0.0f;
+        T* out = (T*)a.out + row * D;
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) out[e * 64 + lane] = (T)(o[i][e] * inv);
+        if (a.lse && lane == 0) a.lse[row] = (m[i] + __builtin_amdgcn_logf(le[i])) * (1.0f / kLog2e);
+    }
+}
+
+template <class T>
+static hipError_t launch_tree_join(const AttnArgs& a, hipStream_t st)
+{
+    const long rows = (long)(a.s.max_q > 0 ? a.s.max_q : 1) * a.G, BR = 32 * tile_waves(a.s.d), rt = (rows + BR - 1) / BR;
+    const dim3 grid(a.s.batch, (unsigned)(a.s.hkv * rt), (unsigned)(BR / (a.s.d <= 128 ? 16 : 8)));
+    switch (a.s.d) {
+    case 64: k_attn_tree_join<T, 64><<<grid, dim3(256), 0, st>>>(a, (int)rt); break;
+    case 128: k_attn_tree_join<T, 128><<<grid, dim3(256), 0, st>>>(a, (int)rt); break;
+    case 192: k_attn_tree_join<T, 192><<<grid, dim3(256), 0, st>>>(a, (int)rt); break;
+    default: k_attn_tree_join<T, 256><<<grid, dim3(256), 0, st>>>(a, (int)rt);
+    }
+    return hipGetLastError();
 }
 
 }  // namespace fc

@@ -327,6 +327,13 @@ struct AttnArgs {
     const unsigned long long* tree_bits;
     const int* tree_pos;
     int tree_words;
+    // The tile form shares trees' work evenly (even != 0): the stages of all sequences' keys, one after
+    // the other, go in equal parts to `even` blocks for each head and tile of rows. The results of a
+    // sequence that several blocks have go to slot (block + sequence) of the head's and tile's `slots`,
+    // each of the form's rows: part_o [hkv, row tiles, slots, rows, d], part_ml [hkv, row tiles, slots,
+    // rows]; ends [batch][2]: the sequence's first and last block.
+    int even, slots;
+    int* ends;
 };
 
 // The bits of the 64 nodes from `node` on (which may lie before the tree or past it).
