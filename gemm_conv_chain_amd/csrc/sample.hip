@@ -31,7 +31,6 @@ constexpr int SR_BATCH = 2048;     // logits a wave takes at a time, 32 a lane
 constexpr int SR_SHORT = 8;        // waves of a block that draws from a row's largest,
 constexpr int SR_LONG = 16;        // and from all of a row
 constexpr int SR_LIST = 64 * SR_SHORT;   // elements in question that a row's largest may be
-constexpr int SR_FEW = 128;        // elements of a bin that are looked at one by one
 constexpr int SR_NUCLEUS = 256;    // logits that a cut by mass alone looks at first
 constexpr double SR_ONE = 0x1p42;  // a weight of 1
 constexpr int SR_NOT_YET = -2;     // in out: the row is k_sample_long's
@@ -120,7 +119,9 @@ __device__ __forceinline__ void lds_max(FC_LDS unsigned* p, unsigned v)
 template <int WAVES, bool ROW> struct Shared {
     double table[32];
     u64 bins[ROW ? WAVES : 1][64 * WAVES];
-    u32x4 few[SR_FEW];
+    static constexpr int FEW = ROW ? 512 : 128;   // elements of a bin that are looked at one by one
+    u32x4 few[FEW];
+    u64 extra[WAVES];
     u32x4 list[ROW ? 1 : SR_LIST];
     int chosen[ROW ? 1 : SR_LIST];    // groups
     u64 wave_mass[WAVES];
@@ -178,6 +179,13 @@ __device__ __forceinline__ float from_key(unsigned k)
 // 2^(slope d / 32) + plus for slope d > -32000: a table of 2^(i / 32) (each entry has its own two of
 // LDS's 64 banks) times 2^(r / 32), |r| <= 1/2, by its Taylor series, whose next term is 2e-15.
 typedef FC_LDS double lds_double;
+// a * b + c to a register of its own (the compiler adds in place, after a copy of each constant).
+__device__ __forceinline__ double fma_to(double a, double b, double c)
+{
+    double d;
+    asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+    return d;
+}
 __device__ __forceinline__ double exp2_down(double d, double slope, double plus, const lds_double* table)
 {
     constexpr double shift = 0x1.8p52;
@@ -186,11 +194,11 @@ __device__ __forceinline__ double exp2_down(double d, double slope, double plus,
     const double r = __builtin_fma(d, slope, shift - zi);
     constexpr double l = 0.693147180559945309417 / 32;
     constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5;
-    double p = __builtin_fma(c5, r, c4);
-    p = __builtin_fma(p, r, c3);
-    p = __builtin_fma(p, r, c2);
-    p = __builtin_fma(p, r, l);
-    p = __builtin_fma(p, r, 1.0);
+    double p = fma_to(c5, r, c4);
+    p = fma_to(p, r, c3);
+    p = fma_to(p, r, c2);
+    p = fma_to(p, r, l);
+    p = fma_to(p, r, 1.0);
     const u64 t = __builtin_bit_cast(u64, table[n & 31]) + ((u64)(unsigned)((n >> 5) << 20) << 32);
     return __builtin_fma(p, __builtin_bit_cast(double, t), plus);
 }
@@ -312,7 +320,8 @@ __device__ __forceinline__ BatchInfo scan_batch(const L* row, int base, int voca
 // What a block does with a row: ROW by all of its logits, else by its largest (of the infos and groups
 // of its batches).
 template <class L, int WAVES, bool ROW> struct Sampler {
-    static constexpr int THREADS = 64 * WAVES, BINS = THREADS;
+    static constexpr int THREADS = 64 * WAVES, BINS = THREADS, FEW = Shared<WAVES, ROW>::FEW;
+    static constexpr int LOOK = sizeof(L) == 2 ? 3 : 2;   // loads on the way where little is done with them
     const SampleArgs& a;
     FC_LDS Shared<WAVES, ROW>& s;
     const L* row;
@@ -363,9 +372,9 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     // f(index, logit, weight()) for lo .. hi - 1, by one wave: lo and, but for the row's end, hi are
     // multiples of 512. -inf for what is past the row's end. Four logits' work together: more take more
     // registers than there are.
-    template <class F> __device__ __forceinline__ void each(int lo, int hi, F&& f) const
+    // U: loads of this step, and as many of the next on the way.
+    template <int U, class F> __device__ __forceinline__ void each(int lo, int hi, F&& f) const
     {
-        constexpr int U = 2;   // loads of this step, and as many of the next on the way
         Eight<L> next[U];
 #pragma unroll
         for (int k = 0; k < U; ++k) next[k] = fetch(row, lo + lane * 8 + k * 512, a.vocab);
@@ -397,12 +406,12 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     // The same as sources of elements: all of the row (a wave has a sixteenth of it), n elements of
     // s.list, n groups' largest (as weights 1).
     __device__ __forceinline__ int part() const { return ((a.vocab + WAVES - 1) / WAVES + 511) / 512 * 512; }
-    struct Whole {
+    template <int U> struct Whole {
         const Sampler& p;
         template <class F> __device__ __forceinline__ void operator()(F&& f) const
         {
             const int per = p.part(), lo = p.wave * per, hi = lo + per < p.a.vocab ? lo + per : p.a.vocab;
-            p.each(lo, hi, f);
+            p.template each<U>(lo, hi, f);
         }
     };
     struct Listed {
@@ -445,9 +454,9 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         return u < 1.0f && g < all ? g : all - 1;
     }
 
-    __device__ __forceinline__ void clear_bins()
+    template <bool ALL = true> __device__ __forceinline__ void clear_bins()   // (ALL false: one copy)
     {
-        if (ROW) {
+        if (ROW && ALL) {
             FC_LDS u32x4* const p = (FC_LDS u32x4*)s.bins;
 #pragma unroll
             for (int k = 0; k < WAVES / 2; ++k) p[k * THREADS + tid] = u32x4{0, 0, 0, 0};
@@ -459,7 +468,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     }
     __device__ __forceinline__ void add_bin(int b, u64 v) { lds_add(&s.bins[ROW ? wave : 0][b], v); }
     // The bin at which the running sum reaches goal, -1 where none does; *before: the sum ahead of it.
-    __device__ __forceinline__ int find_bin(u64 goal, u64* before)
+    template <bool ALL = true> __device__ __forceinline__ int find_bin(u64 goal, u64* before)
     {
         __syncthreads();
         if (tid == 0) {
@@ -467,8 +476,9 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             s.key_lo = ~0u;
             s.key_hi = 0;
         }
+        if (tid < WAVES) s.extra[tid] = 0;
         u64 v = s.bins[0][tid];
-        if (ROW)
+        if (ROW && ALL)
 #pragma unroll
             for (int k = 1; k < WAVES; ++k) v += s.bins[ROW ? k : 0][tid];
         u64 upto = wave_scan(v);
@@ -531,7 +541,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             const int per = ((hi - lo + WAVES - 1) / WAVES + 511) / 512 * 512;
             const int z = lo + (wave + 1) * per < hi ? lo + (wave + 1) * per : hi;
             u64 sum = 0;
-            if (!known) each(lo + wave * per, z, [&](int i, float x, auto&& weight) { sum += w(i, x, weight); });
+            if (!known) each<2>(lo + wave * per, z, [&](int i, float x, auto&& weight) { sum += w(i, x, weight); });
             sum = known ? mine : wave_sum(sum);
             known = false;
             if (lane == 0) s.wave_mass[wave] = sum;
@@ -570,12 +580,55 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         if (lane == 0 && rest) add_bin(BINS - 1, rest);
     }
 
+    // Of n elements, a thread each (`live`), with keys lo .. hi, the one at which the running sum of their
+    // weights in falling order reaches goal, to s.cut_x and s.cut_i: by histograms until at most 64
+    // are left, or equal ones, and of these each looks at all.
+    __device__ __forceinline__ void pick_few(Entry e, bool live, int n, u64 goal, unsigned lo, unsigned hi)
+    {
+        const unsigned key = order_key(__builtin_bit_cast(float, (unsigned)e[0]));
+        const u64 w = high_pair(e);
+        while (n > 64 && lo < hi) {
+            int shift = 0;
+            while ((hi - lo) >> shift >= BINS) ++shift;
+            __syncthreads();   // everyone has read what the counts are reset of
+            clear_bins<false>();
+            if (live) lds_add(&s.bins[0][(hi - key) >> shift], w);
+            u64 ahead;
+            const int b = find_bin<false>(goal, &ahead);
+            goal -= ahead;
+            live = live && (int)((hi - key) >> shift) == b;
+            if (live) {
+                s.few[lds_add(&s.n_few, 1u)] = e;
+                lds_min(&s.key_lo, key);
+                lds_max(&s.key_hi, key);
+            }
+            __syncthreads();
+            n = s.n_few;
+            lo = s.key_lo;
+            hi = s.key_hi;
+        }
+        if (live) {
+            u64 m = 0;
+#pragma unroll 4
+            for (int j = 0; j < n; ++j) {
+                const Entry y = s.few[j];
+                m += before(y, e) ? high_pair(y) : 0;
+            }
+            if (m < goal && m + w >= goal) {
+                s.cut_x = __builtin_bit_cast(float, (unsigned)e[0]);
+                s.cut_i = e[1];
+            }
+        }
+        __syncthreads();
+    }
+
     // The last element that stays, in s.cut_x and s.cut_i: the goal-th in falling order, or (MASS)
     // that at which the mass reaches goal; `share` > 0: that share of the whole mass.  False where there are not so many.  `tie(many, x)`: the
     // index of the many-th element that is x.  Of a row, *mine: the sum of this wave's part in the bins
-    // before the cut's, whose largest value may be s.cut_top.
-    template <bool MASS, class S, class T>
-    __device__ __forceinline__ bool cut_at(const S& source, u64 goal, float share, T&& tie, u64* mine)
+    // before the cut's, whose largest value may be s.cut_top; or (cut_top -inf) with what stays of that.
+    // `look`: the source, for passes that do little.
+    template <bool MASS, class S, class Q, class T>
+    __device__ __forceinline__ bool cut_at(const S& source, const Q& look, u64 goal, float share, T&& tie, u64* mine)
     {
         fill_bins<MASS>(source, [&](float x) { return bin(x); });
         if (ROW && share > 0.0f) {
@@ -596,10 +649,10 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         }
         goal -= ahead;
         unsigned lo = edge(b), hi = edge(b - 1) - 1;   // keys of the elements in question, the bin's at first
-        for (;;) {
+        for (bool all = true;; all = false) {   // all: of the bin's elements
             const float xa = from_key(lo), xb = from_key(hi);
             unsigned least = ~0u, most = 0;
-            source([&](int i, float x, auto&& weight) {
+            look([&](int i, float x, auto&& weight) {
                 if (!(x >= xa && x <= xb)) return;
                 const unsigned key = order_key(x);
                 least = key < least ? key : least;
@@ -609,7 +662,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
                 unsigned at = 0;
                 if (lane == first) at = lds_add(&s.n_few, (unsigned)__builtin_popcountll(here));
                 at = __builtin_amdgcn_readlane(at, first) + __builtin_popcountll(here & ((1ull << lane) - 1));
-                if (at < SR_FEW) {
+                if (at < FEW) {
                     u64 w = 1;
                     if constexpr (MASS) w = weight();
                     s.few[at] = entry(x, i, w);
@@ -621,20 +674,19 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             }
             __syncthreads();
             const int few = s.n_few;
-            if (few <= SR_FEW) {   // one by one: what lies before each
-                if (tid < few) {
-                    const Entry e = s.few[tid];
-                    u64 m = 0;
-                    for (int j = 0; j < few; ++j) {
-                        const Entry y = s.few[j];
-                        m += before(y, e) ? high_pair(y) : 0;
+            if (few <= FEW) {
+                const bool mine_too = tid < few;
+                const Entry e = mine_too ? s.few[tid] : Entry{0, 0, 0, 0};
+                pick_few(e, mine_too, few, goal, s.key_lo, s.key_hi);
+                if (ROW && MASS && all) {   // those that stay, to their parts' sums
+                    if (mine_too) {
+                        const int i = e[1];
+                        if (stays(__builtin_bit_cast(float, (unsigned)e[0]), i, s.cut_x, s.cut_i)) lds_add(&s.extra[i / part()], high_pair(e));
                     }
-                    if (m < goal && m + high_pair(e) >= goal) {
-                        s.cut_x = __builtin_bit_cast(float, (unsigned)e[0]);
-                        s.cut_i = e[1];
-                    }
+                    if (tid == 0) s.cut_top = kNegInf;
+                    __syncthreads();
+                    *mine += s.extra[wave];
                 }
-                __syncthreads();
                 return true;
             }
             lo = s.key_lo;
@@ -675,18 +727,18 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         u64 ahead;
         const int b = find_bin(goal + 1, &ahead);
         goal -= ahead;
-        // (a bin has 2^shift indices: up to SR_FEW of the list here, else they are searched in the list)
+        // (a bin has 2^shift indices: up to FEW of the list here, else they are searched in the list)
         const bool mine = own && (int)(e[1] >> shift) == b;
         unsigned at = 0;
         if (mine) {
             at = lds_add(&s.n_few, 1u);
-            if (at < SR_FEW) s.few[at] = entry(0.0f, e[1], own);
+            if (at < FEW) s.few[at] = entry(0.0f, e[1], own);
         }
         __syncthreads();
         const int few = s.n_few;
         if (mine) {
             u64 m = 0;
-            if (few <= SR_FEW) {
+            if (few <= FEW) {
                 for (int j = 0; j < few; ++j) {
                     const Entry y = s.few[j];
                     m += y[1] < e[1] ? high_pair(y) : 0;
@@ -709,13 +761,14 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     {
         float cut_x = kNegInf;
         int cut_i = 0x7fffffff;
-        const Whole source{*this};
+        const Whole<2> source{*this};
+        const Whole<LOOK> look{*this};
         u64 mine = 0;
         const auto tie = [&](u64 many, float x) {
             return locate(many - 1, false, 0.0f, false, 0, [&](int, float y, auto&&) { return y == x ? 1ull : 0ull; });
         };
         if (set.k > 0) {
-            if (cut_at<false>(source, set.k, 0.0f, tie, &mine)) {
+            if (cut_at<false>(look, look, set.k, 0.0f, tie, &mine)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             }
@@ -727,7 +780,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
                 source([&](int i, float x, auto&& weight) { left += stays(x, i, cut_x, cut_i) ? weight() : 0; });
                 left = (u64)__builtin_ceil((double)set.p * (double)block_sum(left));
             }
-            if (cut_at<true>(source, left, set.k > 0 ? 0.0f : set.p, tie, &mine)) {
+            if (cut_at<true>(source, look, left, set.k > 0 ? 0.0f : set.p, tie, &mine)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             }
@@ -735,10 +788,10 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         }
         // Cut by mass alone: the parts' sums before the cut's bin are there, that bin's are added.
         const bool known = set.k == 0 && set.least == 0 && cut_x > kNegInf;
-        if (known) {
-            const float top = s.cut_top;
+        const float top = s.cut_top;
+        if (known && top > kNegInf) {
             u64 sum = 0;
-            source([&](int i, float x, auto&& weight) {
+            look([&](int i, float x, auto&& weight) {
                 if (x <= top && stays(x, i, cut_x, cut_i)) sum += weight();
             });
             mine += wave_sum(sum);
@@ -764,7 +817,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             return index_at(many - 1, n, [&](int, float z, u64) { return z == y ? 1ull : 0ull; });
         };
         if (set.k > 0) {
-            if (cut_at<false>(source, set.k, 0.0f, tie, nullptr)) {
+            if (cut_at<false>(source, source, set.k, 0.0f, tie, nullptr)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             }
@@ -772,7 +825,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         }
         if (set.p < 1.0f) {
             if (set.k > 0) all = block_sum(stays(x, e[1], cut_x, cut_i) ? w : 0);
-            if (cut_at<true>(source, (u64)__builtin_ceil((double)set.p * (double)all), 0.0f, tie, nullptr)) {
+            if (cut_at<true>(source, source, (u64)__builtin_ceil((double)set.p * (double)all), 0.0f, tie, nullptr)) {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             } else if (!floored) {
@@ -799,7 +852,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         if (first <= (unsigned)ngroups) {
             const Tops<G> source{*this, groups, ngroups};
             if (again) {
-                if (cut_at<false>(source, first, 0.0f, [](u64, float) { return 0; }, nullptr)) floor = s.cut_x;
+                if (cut_at<false>(source, source, first, 0.0f, [](u64, float) { return 0; }, nullptr)) floor = s.cut_x;
             } else {
                 fill_bins<false>(source, [&](float x) { return bin(x); });
                 u64 ahead;
@@ -1013,7 +1066,12 @@ __global__ __launch_bounds__(64 * SR_LONG) void k_sample_long(SampleArgs a)
         filled = true;
         Sampler<L, SR_LONG, true> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f};
         float top = kNegInf;
-        typename Sampler<L, SR_LONG, true>::Whole{w}([&](int, float x, auto&&) { top = fmaxf(top, x); });
+        if (a.info) {
+            const BatchInfo* const infos = (const BatchInfo*)a.info + r * a.batches;
+            for (int b = threadIdx.x; b < a.batches; b += 64 * SR_LONG) top = fmaxf(top, info_max(infos[b]));
+        } else {
+            typename Sampler<L, SR_LONG, true>::template Whole<2>{w}([&](int, float x, auto&&) { top = fmaxf(top, x); });
+        }
         top = wave_top(top);
         if (lane == 0) s.wave_x[wave] = top;
         __syncthreads();
@@ -1127,6 +1185,7 @@ hipError_t run_sample(int dtype, const void* logits, long rows, int vocab, long 
 {
     SampleArgs a{logits, stride, u, temperatures, top_ks, top_ps, min_ps, temperature, top_p, min_p, top_k, vocab, rows, out,
                  (vocab + SR_BATCH - 1) / SR_BATCH, workspace, nullptr};
+    if (at_once(vocab)) a.info = nullptr;   // (a workspace that is not needed may be given)
     a.groups = reinterpret_cast<float*>((BatchInfo*)workspace + rows * a.batches);
     if (dtype == DT_F16) return launch_sample<half_t>(a, st);
     return dtype == DT_BF16 ? launch_sample<bf16_t>(a, st) : launch_sample<float>(a, st);
