@@ -40,14 +40,15 @@ def make_weights(seed=0, device="cuda"):
                 w0=w(HIDDEN, FFN), b0=b(FFN), w1=w(FFN, HIDDEN), b1=b(HIDDEN), turns=turns, mscale=mscale)
 
 
-def layer(x, p, cache, table, cu_q, kv_lens, max_q, max_kv):
+def layer(x, p, cache, table, cu_q, kv_lens, max_q, max_kv, tree=None):
     """x [tokens, HIDDEN] -> the same, its keys and values appended to the cache;
-    returns (result, what was computed on the way)."""
+    returns (result, what was computed on the way).  ``tree``: fc.tree_plan's, if the
+    new tokens are a tree of drafts."""
     qkv = fc.gemm_bias_act(x, p["wqkv"], p["bqkv"])
     rows = qkv.view(-1, HQ + 2 * HKV, D)
     q = fc.kv_append(rows[:, HQ:HQ + HKV], rows[:, HQ + HKV:], *cache, table, cu_q, kv_lens, turns=p["turns"],
-                     mscale=p["mscale"], q=rows[:, :HQ], max_q=max_q)
-    attn = fc.chain_attn(q, *cache, table, cu_q, kv_lens, max_q=max_q, max_kv=max_kv)
+                     mscale=p["mscale"], q=rows[:, :HQ], max_q=max_q, positions=None if tree is None else tree[1])
+    attn = fc.chain_attn(q, *cache, table, cu_q, kv_lens, max_q=max_q, max_kv=max_kv, tree=tree)
     h = x + fc.gemm_bias_act(attn.view(-1, HQ * D), p["wo"], None)
     mlp = fc.chain_gemm2(h, p["w0"], p["b0"], p["w1"], p["b1"], act="gelu_tanh")
     return h + mlp, dict(qkv=qkv, q=q, attn=attn, h=h, mlp=mlp)
