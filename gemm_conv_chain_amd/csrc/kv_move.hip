@@ -18,14 +18,30 @@ struct KeepArgs {
     float* scales;
     const int *table, *cu_q, *kv_lens, *keep, *kept;
     int max_keep;
+    int staged;                         // tokens that a block holds at a time
     size_t layer_codes, layer_scales;   // bytes and scales of a layer
     KvShape s;
     FastDiv units, by_d;                // d / 16, d
 };
 
+constexpr int KEEP_PAGES = 4;   // that a block writes at a time
+
+// A token's source: page (or -1), place in it, scales; and which of the pages it goes to.
+struct alignas(16) Source {
+    int page;
+    short at, to;
+    float scale[2];
+};
+struct alignas(16) KeepShared {
+    unsigned now[KEEP_PAGES][2];   // bits of the pages' new scales
+    float held[KEEP_PAGES][2];
+    int id[KEEP_PAGES];
+    unsigned bad, moves;
+};
+
 // One block a (sequence, kv head, layer).  Tokens only ever move to lower slots, a page's
-// tokens come from it and from later ones: the pages are taken in order, each one's tokens
-// gathered into LDS before any byte of it changes.
+// tokens come from it and from later ones: as many pages as there is room for are taken at a
+// time, in order, their tokens gathered into LDS before any byte of them changes.
 // A scale is a power of two, so that the codes of a page whose scale grows, and those that
 // come from a smaller one, are rounded once more only where they become subnormal.
 __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
@@ -40,10 +56,12 @@ __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
     const int kv_len = a.kv_lens[b], m = a.kept[b], start = kv_len - n;
     if (m <= 0 || m > n || m > a.max_keep || kv_len < n || kv_len > s.page * s.table_stride) return;
     const int* const list = a.keep + (size_t)b * a.max_keep;
-    extern __shared__ __align__(16) uint8_t lds[];      // two scales, two flags, then [side][token][d]
-    unsigned* const top = reinterpret_cast<unsigned*>(lds);
-    uint8_t* const staged = lds + 16;
-    if (tid < 2) top[2 + tid] = 0;
+    extern __shared__ __align__(16) uint8_t lds[];      // KeepShared, the sources, then [side][token][d]
+    KeepShared& sh = *reinterpret_cast<KeepShared*>(lds);
+    Source* const sources = reinterpret_cast<Source*>(lds + sizeof(KeepShared));
+    uint8_t* const sk = lds + sizeof(KeepShared) + sizeof(Source) * a.staged;
+    uint8_t* const sv = sk + a.staged * D;
+    if (tid == 0) sh.bad = sh.moves = 0;
     __syncthreads();
     bool bad = false, moves = false;
     for (int i = tid; i < m; i += 256) {
@@ -51,40 +69,58 @@ __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
         bad |= k <= before || k >= n;
         moves |= k != i;
     }
-    if (bad) top[2] = 1;
-    if (moves) top[3] = 1;
+    if (bad) sh.bad = 1;
+    if (moves) sh.moves = 1;
     __syncthreads();
-    if (top[2] || !top[3]) return;
+    if (sh.bad || !sh.moves) return;
 
-    for (int p = start / s.page; p <= (start + m - 1) / s.page; ++p) {
-        const int slot0 = p * s.page;
-        const int i0 = slot0 > start ? slot0 - start : 0, i1 = slot0 + s.page - start < m ? slot0 + s.page - start : m;
-        const int cnt = i1 - i0, id = page_id(a.table, s, b, p);
-        if (id < 0) continue;
-        float* const scale = scales + ((size_t)id * s.hkv + h) * 2;
-        const float held[2] = {scale[0], scale[1]};
-        if (tid < 2) top[tid] = 0;
-        __syncthreads();
-        for (int i = tid; i < cnt; i += 256) {
-            const int from = page_id(a.table, s, b, (start + list[i0 + i]) / s.page);
-            if (from < 0) continue;
-#pragma unroll
-            for (int side = 0; side < 2; ++side)   // (positive: they order as integers)
-                atomicMax(&top[side], __builtin_bit_cast(unsigned, scales[((size_t)from * s.hkv + h) * 2 + side]));
+    const auto scale_at = [&](int page, int side) { return scales + ((size_t)page * s.hkv + h) * 2 + side; };
+    const auto k_at = [&](int page, int at, int u) {
+        return codes + side_base(page, h, 0, s) + (at >> 4) * 16 * D + u * 256 + (at & 15) * 16;
+    };
+    const auto v_at = [&](int page, int at, int dim) {
+        return codes + side_base(page, h, 1, s) + (size_t)((at >> 4) * D + dim) * 16 + (at & 15);
+    };
+    const int last = (start + m - 1) / s.page;
+    for (int p = start / s.page, i0 = 0; p <= last;) {
+        // pages p .. p + pages - 1, tokens i0 .. i0 + cnt - 1
+        const auto upto = [&](int q) { return min(m, (q + 1) * s.page - start); };
+        int pages = 1;
+        while (pages < KEEP_PAGES && p + pages <= last && upto(p + pages) - i0 <= a.staged) ++pages;
+        const int cnt = upto(p + pages - 1) - i0;
+        Source src{-1, 0, 0, {0.0f, 0.0f}};
+        if (tid < cnt) {   // (at most a.staged, and that at most 256)
+            const int slot = start + list[i0 + tid];
+            src.page = page_id(a.table, s, b, slot / s.page);
+            src.at = (short)(slot % s.page);
+            src.to = (short)((start + i0 + tid) / s.page - p);
+            if (src.page >= 0) {
+                src.scale[0] = *scale_at(src.page, 0);
+                src.scale[1] = *scale_at(src.page, 1);
+            }
+            sources[tid] = src;
+        }
+        if (tid < 2 * pages) {
+            const int q = tid >> 1, side = tid & 1, id = page_id(a.table, s, b, p + q);
+            const float held = id >= 0 ? *scale_at(id, side) : 0.0f;
+            sh.id[q] = id;
+            sh.held[q][side] = held;
+            sh.now[q][side] = __builtin_bit_cast(unsigned, held);
         }
         __syncthreads();
-        float now[2];
+        if (src.page >= 0)
 #pragma unroll
-        for (int side = 0; side < 2; ++side) now[side] = fmaxf(held[side], __builtin_bit_cast(float, top[side]));
-        uint8_t* const sk = staged;
-        uint8_t* const sv = staged + (size_t)cnt * D;
+            for (int side = 0; side < 2; ++side)   // (positive: they order as integers)
+                atomicMax(&sh.now[src.to][side], __builtin_bit_cast(unsigned, src.scale[side]));
+        __syncthreads();
+        const auto now = [&](int q, int side) { return __builtin_bit_cast(float, sh.now[q][side]); };
         for (int e = tid; e < cnt * units; e += 256) {
-            const int t = a.units.div(e), u = e - t * units, slot = start + list[i0 + t], at = slot % s.page;
-            const int from = page_id(a.table, s, b, slot / s.page);
+            const int t = a.units.div(e), u = e - t * units;
+            const Source from = sources[t];
             u32x4 w = {0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu};
-            if (from >= 0) {
-                w = *reinterpret_cast<const u32x4*>(codes + side_base(from, h, 0, s) + (at >> 4) * 16 * D + u * 256 + (at & 15) * 16);
-                const float ratio = scales[((size_t)from * s.hkv + h) * 2] / now[0];
+            if (from.page >= 0) {
+                w = *reinterpret_cast<const u32x4*>(k_at(from.page, from.at, u));
+                const float ratio = from.scale[0] / now(from.to, 0);
                 if (ratio != 1.0f) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[j] = recode_codes(w[j], ratio);
@@ -92,61 +128,69 @@ __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
             }
             *reinterpret_cast<u32x4*>(sk + t * D + u * 16) = w;
         }
-        for (int e = tid; e < cnt * D; e += 256) {
-            const int t = a.by_d.div(e), dim = e - t * D, slot = start + list[i0 + t], at = slot % s.page;
-            const int from = page_id(a.table, s, b, slot / s.page);
-            unsigned w = 0;
-            if (from >= 0) {
-                w = codes[side_base(from, h, 1, s) + (size_t)((at >> 4) * D + dim) * 16 + (at & 15)];
-                const float ratio = scales[((size_t)from * s.hkv + h) * 2 + 1] / now[1];
-                if (ratio != 1.0f) w = recode_codes(w, ratio);
+        for (int e0 = tid; e0 < cnt * D; e0 += 4 * 256) {   // four bytes on the way at a time
+            unsigned w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = e0 + 256 * j, t = a.by_d.div(e);
+                w[j] = e < cnt * D && sources[t].page >= 0 ? *v_at(sources[t].page, sources[t].at, e - t * D) : 0;
             }
-            sv[t * D + dim] = (uint8_t)w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int e = e0 + 256 * j, t = a.by_d.div(e);
+                if (e >= cnt * D) continue;
+                const float ratio = sources[t].page >= 0 ? sources[t].scale[1] / now(sources[t].to, 1) : 1.0f;
+                sv[e] = (uint8_t)(ratio != 1.0f ? recode_codes(w[j], ratio) : w[j]);
+            }
         }
         __syncthreads();
-        // earlier tokens of the page, where its scale grows
-        const int lo = start > slot0 ? start - slot0 : 0;
+        // earlier tokens of the first page, where its scale grows
+        const int lo = start - p * s.page, id0 = sh.id[0];
+        if (lo > 0 && id0 >= 0) {
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            if (lo == 0 || !(now[side] > held[side])) continue;
-            const float ratio = held[side] / now[side];
-            uint8_t* const base = codes + side_base(id, h, side, s);
-            if (side == 0) {
-                for (int e = tid; e < lo * units; e += 256) {
-                    const int t = a.units.div(e), u = e - t * units;
-                    u32x4* q = reinterpret_cast<u32x4*>(base + (t >> 4) * 16 * D + u * 256 + (t & 15) * 16);
-                    u32x4 w = *q;
+            for (int side = 0; side < 2; ++side) {
+                const float held = sh.held[0][side];
+                if (!(now(0, side) > held)) continue;
+                const float ratio = held / now(0, side);
+                uint8_t* const base = codes + side_base(id0, h, side, s);
+                if (side == 0) {
+                    for (int e = tid; e < lo * units; e += 256) {
+                        const int t = a.units.div(e), u = e - t * units;
+                        u32x4* q = reinterpret_cast<u32x4*>(base + (t >> 4) * 16 * D + u * 256 + (t & 15) * 16);
+                        u32x4 w = *q;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) w[j] = recode_codes(w[j], ratio);
-                    *q = w;
-                }
-            } else {
-                for (int e = tid; e < ((lo + 15) >> 4) * D; e += 256) {
-                    const int left = lo - a.by_d.div(e) * 16;   // tokens of the block that were there
-                    u32x4* q = reinterpret_cast<u32x4*>(base + (size_t)e * 16);
-                    u32x4 w = *q;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = left - 4 * j;
-                        const unsigned mk = k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
-                        w[j] = (recode_codes(w[j], ratio) & mk) | (w[j] & ~mk);
+                        for (int j = 0; j < 4; ++j) w[j] = recode_codes(w[j], ratio);
+                        *q = w;
                     }
-                    *q = w;
+                } else {
+                    for (int e = tid; e < ((lo + 15) >> 4) * D; e += 256) {
+                        const int left = lo - a.by_d.div(e) * 16;   // tokens of the block that were there
+                        u32x4* q = reinterpret_cast<u32x4*>(base + (size_t)e * 16);
+                        u32x4 w = *q;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int k = left - 4 * j;
+                            const unsigned mk = k >= 4 ? ~0u : (k <= 0 ? 0u : (1u << (8 * k)) - 1u);
+                            w[j] = (recode_codes(w[j], ratio) & mk) | (w[j] & ~mk);
+                        }
+                        *q = w;
+                    }
                 }
             }
+            __syncthreads();   // the vectors are written before single bytes of them
         }
-        __syncthreads();   // the vectors are written before single bytes of them
         for (int e = tid; e < cnt * units; e += 256) {
-            const int t = a.units.div(e), u = e - t * units, at = start + i0 + t - slot0;
-            *reinterpret_cast<u32x4*>(codes + side_base(id, h, 0, s) + (at >> 4) * 16 * D + u * 256 + (at & 15) * 16) =
-                *reinterpret_cast<const u32x4*>(sk + t * D + u * 16);
+            const int t = a.units.div(e), u = e - t * units, q = sources[t].to, at = start + i0 + t - (p + q) * s.page;
+            if (sh.id[q] >= 0) *reinterpret_cast<u32x4*>(k_at(sh.id[q], at, u)) = *reinterpret_cast<const u32x4*>(sk + t * D + u * 16);
         }
         for (int e = tid; e < cnt * D; e += 256) {
-            const int t = a.by_d.div(e), dim = e - t * D, at = start + i0 + t - slot0;
-            codes[side_base(id, h, 1, s) + (size_t)((at >> 4) * D + dim) * 16 + (at & 15)] = sv[t * D + dim];
+            const int t = a.by_d.div(e), q = sources[t].to, at = start + i0 + t - (p + q) * s.page;
+            if (sh.id[q] >= 0) *v_at(sh.id[q], at, e - t * D) = sv[e];
         }
-        if (tid < 2) scale[tid] = now[tid];
+        if (tid < 2 * pages && sh.id[tid >> 1] >= 0) *scale_at(sh.id[tid >> 1], tid & 1) = now(tid >> 1, tid & 1);
         __syncthreads();   // LDS is free again
+        p += pages;
+        i0 += cnt;
     }
 }
 
@@ -195,7 +239,10 @@ hipError_t run_kv_keep(uint8_t* codes, float* scales, int layers, const int* tab
     a.s = s;
     a.units = FastDiv::make(s.d / 16);
     a.by_d = FastDiv::make(s.d);
-    const int lds = 16 + 2 * s.d * (max_keep < s.page ? max_keep : s.page);
+    // a page's worth, or a few small pages'
+    const int room = s.page < 32 ? 32 : s.page;
+    a.staged = max_keep < room ? max_keep : room;
+    const int lds = (int)sizeof(KeepShared) + (2 * s.d + (int)sizeof(Source)) * a.staged;
     k_kv_keep<<<dim3(s.batch, s.hkv, layers), dim3(256), lds, st>>>(a);
     return hipGetLastError();
 }
