@@ -1426,6 +1426,8 @@ class KvPages:
         row, now = self._rows[seq], self._lens[seq]
         if length < now:
             raise ValueError("sequence %r has %d tokens, cannot grow to %d" % (seq, now, length))
+        if length == now:
+            return []
         first = now // self.page                          # the first page that is written
         shared = [i for i in range(first, min(len(row), -(-length // self.page))) if self.refs[row[i]] > 1]
         more = max(0, -(-length // self.page) - len(row))

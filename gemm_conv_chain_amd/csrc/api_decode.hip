@@ -148,6 +148,13 @@ fc_status sample_tokens(const void* logits, int32_t dtype, int64_t rows, int32_t
     if (!aligned(u, 4) || !aligned(out, 4) || !aligned(g.temperatures, 4) || !aligned(g.top_ks, 4) || !aligned(g.top_ps, 4) ||
         !aligned(g.min_ps, 4))
         return fail(FC_E_ALIGN, "u, out and the settings' arrays must be 4-byte aligned");
+    // (a token, or the mark of a row that is not done, would be read as a setting)
+    const auto meets_out = [&](const void* p) {
+        const uintptr_t x = (uintptr_t)p, y = (uintptr_t)out, bytes = (uintptr_t)rows * 4;
+        return p && x < y + bytes && y < x + bytes;
+    };
+    if (meets_out(u) || meets_out(g.temperatures) || meets_out(g.top_ks) || meets_out(g.top_ps) || meets_out(g.min_ps))
+        return fail(FC_E_ARG, "out overlaps u or a setting's array");
     const int64_t need = fc::sample_space(rows, vocab);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(workspace ? FC_E_SHAPE : FC_E_NULL, "a workspace of %lld bytes is required, got %lld", (long long)need,

@@ -124,6 +124,10 @@ def test_sample_refusals(L):
     assert sample(L, k=-1) == E_ARG
     for v in (-0.1, 1.1, nan):
         assert sample(L, p=v) == E_ARG and sample(L, m=v) == E_ARG
+    # the tokens may not be written over what is still read
+    assert sample(L, u=0x20000, out=0x20008) == E_ARG and sample(L, u=0x20008, out=0x20000) == E_ARG
+    for i in range(4):
+        assert sample(L, u=0x30000, out=0x20000, arrays=tuple(0x20000 if i == j else None for j in range(4))) == E_ARG
     # a row's own settings stand in for the value for all
     assert sample(L, rows=0, t=nan, arrays=(0x10000, None, None, None)) == OK
     n = ctypes.c_int64(-1)

@@ -61,6 +61,19 @@ def test_plan_of_the_longest_chain_and_past_it(fc):
     assert bits[:66].eq(0).all() and pos[:66].eq(4).all() and bits[66:, 0].tolist() == [1, 2, 4, 8]
 
 
+@pytest.mark.parametrize("reach", [1, 64, 65, 200, 4000])
+def test_plan_across_words(fc, reach):
+    """Parents in the same 64 nodes, in those before, and far away."""
+    print("case plan reach", reach, flush=True)
+    rng = random.Random(reach)
+    new = [1500, 64, 65, 700]
+    trees = [grow(rng, n, reach) for n in new]
+    bits, pos = fc.tree_plan(i32(sum(trees, [])).cuda(), cumulative(new).cuda(), i32(new).cuda(), max_q=1500)
+    seen = [D.ancestors(t) for t in trees]
+    assert bits.tolist() == [r for s in seen for r in D.words_of(s, 24)]
+    assert pos.tolist() == [len(s) - 1 for ss in seen for s in ss]
+
+
 @pytest.mark.parametrize("new", SIZES, ids=lambda v: "x".join(map(str, v[:5])))
 @pytest.mark.parametrize("most", [None, 3])
 def test_accept(fc, new, most):

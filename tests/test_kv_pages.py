@@ -46,6 +46,14 @@ def test_a_fork_at_a_page_border_copies_nothing():
     assert p.grow(2, 40) == [] and p.held(2) == [0, 1, 2] and p.grow(1, 33) == [] and p.held(1) == [0, 1, 3]
 
 
+def test_nothing_to_write_copies_nothing():
+    p = fc.KvPages(1, 16)
+    p.add("a")
+    p.grow("a", 9)
+    p.fork("a", "b")
+    assert p.grow("b", 9) == [] and p.held("b") == [0] and p.refs == [2]
+
+
 def test_too_few_pages_change_nothing():
     p = fc.KvPages(3, 16)
     p.add("a")
