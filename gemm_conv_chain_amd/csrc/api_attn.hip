@@ -218,7 +218,14 @@ struct TreeTiles {
 // As many blocks as the machine holds at once, two a CU for heads of 64 and 128 and one for larger
 // ones (registers and shared memory), with no less than eight stages each.  More tiles than four
 // times that need no sharing.  (The prefix sums over sequences in each block are for thousands of
-// these at most.)
+// these at most.)  Measured (us, by blocks a CU):
+//   32 trees of 26, to 8192 keys, 32 / 8 heads of 128    1: 187   2: 122   3: 150   4: 138
+//   2 of 60, to 100001 keys, 32 / 4                      1: 297   2: 234   3: 276
+//   16 of 32, to 8192 keys, 32 / 8                       1: 118   2: 96    4: 114
+//   4 of 64, to 32768 keys, 32 / 8                       1: 203   2: 159   4: 176
+// The rows form, by the rule of plan_attn, against this one: 8 trees of 16 (64 rows a kv head) 56
+// against 52, one of 16 21 against 32, 32 of 8 over 4096 keys 54 against 67, 16 of 16 with heads of
+// 256 92 against 275.
 TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
 {
     const int64_t G = s->hq / s->hkv, rows = s->d <= 128 ? 128 : 256, keys = s->d <= 192 ? 64 : 32;

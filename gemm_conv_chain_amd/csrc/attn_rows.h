@@ -40,7 +40,8 @@ __device__ __forceinline__ u32x4 load_nt(global_u8* p)
 
 // TREE: the new tokens are nodes of a tree of drafts.  All see the slots before the
 // tree, and of the tree's those whose bit is set; distances go by the nodes'
-// positions.  Only the last tiles hold nodes, so that the loop stays as it is.
+// positions.  Only the last tiles hold nodes, so that the loop stays as it is.  (A tree of 8
+// nodes over 513 keys, 8 / 2 heads of 64: 11.2 us, a causal call of as many 10.4.)
 template <class T, int D, int NT, int MODE, bool TREE>
 __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_attn_rows(AttnArgs a, int row_blocks)
 {

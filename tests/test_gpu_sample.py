@@ -220,3 +220,18 @@ def test_shares_come_out_as_drawn(fc):
     share = torch.softmax(x.double() / 0.9, 0)
     many = torch.bincount(got.cpu().long(), minlength=5)
     assert (many - share * n).abs().max() <= 1          # a border falls inside one step of 1 / n
+
+
+@pytest.mark.parametrize("vocab", [6000, 12000, 20000, 32768])
+def test_a_row_is_drawn_alike_in_any_company(fc, vocab):
+    """However many rows there are, and so whichever kernels take them."""
+    print("case company", vocab, flush=True)
+    g = torch.Generator()
+    g.manual_seed(vocab)
+    x = (3 * torch.randn((4, vocab), generator=g)).half().cuda()
+    u = torch.rand(4, generator=g).cuda()
+    for st in ((1.0, 0, 1.0, 0.0), (0.9, 40, 0.95, 0.0), (1.2, 0, 0.9, 0.0), (0.0, 0, 1.0, 0.0)):
+        want = fc.sample_tokens(x, u, *st)
+        assert want.ge(0).all()
+        for n in (50, 150):
+            assert torch.equal(fc.sample_tokens(x.repeat(n, 1), u.repeat(n), *st), want.repeat(n)), (st, n)
