@@ -1196,7 +1196,7 @@ def tree_plan(parents, cu_q, kv_lens, max_q=None):
     words = -(-_bound(max_q, T) // 64)
     dev = parents.get_device()
     _one_device(dev, (cu_q, kv_lens))
-    bits = torch.empty((T, words), dtype=torch.int64, device=parents.device)
+    bits = parents.new_empty((T, words), dtype=torch.int64)
     positions = torch.empty_like(parents)
     s = _call(dev, lib().tree_plan, parents.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), B, T, words, bits.data_ptr(),
               positions.data_ptr(), _raw_stream(dev))
@@ -1212,7 +1212,6 @@ def tree_accept(parents, drafted, targets, cu_q, kv_lens, max_q=None):
     choice there, of ``sample_tokens``), until there is none.  ``keep``: the nodes passed, rising,
     -1 behind them; ``kept``: how many; ``next``: the target of the last; ``lens``: the
     sequence's length with them."""
-    torch = _torch()
     T, = _ndim(parents, "parents", 1)
     B, = _ndim(kv_lens, "kv_lens", 1)
     _indices(((parents, "parents"), (drafted, "drafted"), (targets, "targets")), (T,))
@@ -1221,9 +1220,8 @@ def tree_accept(parents, drafted, targets, cu_q, kv_lens, max_q=None):
     most = _bound(max_q, T)
     dev = parents.get_device()
     _one_device(dev, (drafted, targets, cu_q, kv_lens))
-    out = torch.empty((B, most + 3), dtype=torch.int32, device=parents.device).view(-1)
-    keep, kept, nxt, lens = (out[:B * most].view(B, most), out[B * most:B * (most + 1)], out[B * (most + 1):B * (most + 2)],
-                             out[B * (most + 2):])
+    keep = parents.new_empty((B, most))
+    kept, nxt, lens = parents.new_empty((3, B)).unbind()
     s = _call(dev, lib().tree_accept, parents.data_ptr(), drafted.data_ptr(), targets.data_ptr(), cu_q.data_ptr(),
               kv_lens.data_ptr(), B, T, most, keep.data_ptr(), kept.data_ptr(), nxt.data_ptr(), lens.data_ptr(),
               _raw_stream(dev))
