@@ -248,7 +248,23 @@ TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
 void plan_tree(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
     plan_attn(s, p, out);
-    if (out->variant != FC_ATTN_TILE) return;
+    if (out->variant != FC_ATTN_TILE) {
+        // A split costs the join's launch and a second pass, 5 to 6 us: it has three steps of 256 keys at
+        // least, and no block waits for a CU (us, by splits; trees of 8, 32 / 8 heads of 128):
+        //   8 over 1000 keys     1: 12.8   2: 15.2   4: 17.8      1 over 513     1: 9.9   2: 13.1   4: 13.1
+        //   2 over 2000          1: 17.5   2: 16.1   3: 15.4      8 over 4096    1: 31.4  2: 26.0   4: 27.4
+        //   1 over 32768         4: 62     8: 43     16: 30       16 over 2000   1: 21.4  2: 26.5   4: 33
+        if (p->splits > 0) return;
+        const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv), per = rows > 16 ? 32 : 16;
+        const int64_t base = (int64_t)(s->batch > 0 ? s->batch : 1) * s->hkv * ((rows + per - 1) / per);
+        const int64_t cus = fc::device_cu_count(), room = (rows > 16 && s->d > 64 ? cus / 2 : cus) / base;
+        const int64_t steps = (key_blocks(s, p, per) + 15) / 16, n = room < steps / 3 ? room : steps / 3;
+        fc_attn_params q = *p;
+        q.variant = FC_ATTN_ROWS;
+        q.splits = (int32_t)(n < 1 ? 1 : n);
+        plan_attn(s, &q, out);
+        return;
+    }
     const TreeTiles t = tree_tiles(s, p);
     const int64_t batch = s->batch > 0 ? s->batch : 1, per = t.even ? (t.even + batch - 1) / batch : 1;
     out->splits = (int32_t)per;

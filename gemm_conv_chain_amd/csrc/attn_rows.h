@@ -40,8 +40,7 @@ __device__ __forceinline__ u32x4 load_nt(global_u8* p)
 
 // TREE: the new tokens are nodes of a tree of drafts.  All see the slots before the
 // tree, and of the tree's those whose bit is set; distances go by the nodes'
-// positions.  Only the last tiles hold nodes, so that the loop stays as it is.  (A tree of 8
-// nodes over 513 keys, 8 / 2 heads of 64: 11.2 us, a causal call of as many 10.4.)
+// positions.  Only the last tiles hold nodes, so that the loop stays as it is. 
 template <class T, int D, int NT, int MODE, bool TREE>
 __global__ __launch_bounds__(64 * AR_WAVES, NT == 1 && D <= 128 ? 2 : 1) void k_attn_rows(AttnArgs a, int row_blocks)
 {
@@ -414,7 +413,13 @@ static hipError_t launch_rows(const AttnArgs& a, hipStream_t st)
 template <class T, int D, int MODE, bool TREE>
 static hipError_t rows_tiles(const AttnArgs& a, hipStream_t st)
 {
-    return (long)a.s.max_q * a.G > 16 ? launch_rows<T, D, 2, MODE, TREE>(a, st) : launch_rows<T, D, 1, MODE, TREE>(a, st);
+    // A tree's 32 rows as two blocks of 16 while that leaves no block waiting for a CU: a block's step is
+    // shorter by a third, and the second reads its keys from the cache (8 nodes over 513 keys, 8 / 2
+    // heads of 64: 12.2 -> 8.6 us; 16 trees of 8 over 2000, 32 / 8 of 128: 28.7 -> 21.4; 32 of these, more
+    // blocks than CUs: 32 against 36).
+    const long rows = (long)a.s.max_q * a.G, blocks = (rows + 31) / 32 * a.s.batch * a.s.hkv * a.nsplit;
+    const bool two = rows > 16 && !(TREE && (D <= 64 ? 1 : 2) * blocks <= device_cu_count());
+    return two ? launch_rows<T, D, 2, MODE, TREE>(a, st) : launch_rows<T, D, 1, MODE, TREE>(a, st);
 }
 
 template <class T, int D, bool TREE>

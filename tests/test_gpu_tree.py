@@ -207,9 +207,10 @@ def test_any_bits(fc, variant, dtype):
 @pytest.mark.parametrize("kw", [dict(splits=1), dict(softcap=30.0, splits=1), dict(window=100), {}, dict(splits=4)], ids=str)
 def test_a_chain_is_causal(fc, variant, kw):
     """A tree of one branch gives the bits that the causal call gives where both take a
-    sequence's keys in one part. With a window both are as 64 bits have it: a causal block begins at
-    its own first query's window, a tree's at its sequence's. So are the tile form's parts, which a
-    tree call cuts by the work of all sequences, a causal one by the longest."""
+    sequence's keys in the same parts. With a window both are as 64 bits have it: a causal block begins at
+    its own first query's window, a tree's at its sequence's. So are calls whose splits the rules of each
+    choose, and the tile form's parts, which a tree call cuts by the work of all sequences, a causal one
+    by the longest."""
     print("case chain", variant, kw, flush=True)
     lens, new = [300, 64, 1000, 9], [40, 64, 5, 9]
     b = batch(6, BF16, lens, new, 8, 2, 128, 32)
@@ -218,7 +219,7 @@ def test_a_chain_is_causal(fc, variant, kw):
     tree = fc.tree_plan(par, g["cu_q"], g["kv_lens"], max_q=64)
     a = fc.chain_attn(**g, max_q=64, variant=variant, **kw)
     t = fc.chain_attn(**g, max_q=64, variant=variant, tree=tree, **kw)
-    if kw.get("splits") == 1 or (variant == "rows" and "window" not in kw):
+    if kw.get("splits") == 1 or (variant == "rows" and "splits" in kw):
         assert torch.equal(t, a)
         return
     out, tol, _, _ = D.attention(**b, bits=tree[0].cpu(), positions=tree[1].cpu(), window=kw.get("window", 0))
