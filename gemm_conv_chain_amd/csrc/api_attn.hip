@@ -223,9 +223,6 @@ struct TreeTiles {
 //   2 of 60, to 100001 keys, 32 / 4                      1: 297   2: 234   3: 276
 //   16 of 32, to 8192 keys, 32 / 8                       1: 118   2: 96    4: 114
 //   4 of 64, to 32768 keys, 32 / 8                       1: 203   2: 159   4: 176
-// The rows form, by the rule of plan_attn, against this one: 8 trees of 16 (64 rows a kv head) 56
-// against 52, one of 16 21 against 32, 32 of 8 over 4096 keys 54 against 67, 16 of 16 with heads of
-// 256 92 against 275.
 TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
 {
     const int64_t G = s->hq / s->hkv, rows = s->d <= 128 ? 128 : 256, keys = s->d <= 192 ? 64 : 32;
@@ -245,30 +242,43 @@ TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
     return t;
 }
 
+// The rows form is for few rows, and for more while its blocks of 32 rows fit the machine at once and
+// read less than 2^20 keys together.  Measured, rows against tile (us; batch / keys / rows of a kv
+// head / kv heads):
+//   d =  64   1 / 16000 / 128 / 4  22 : 36    16 / 1000 / 128 / 4  15 : 31    64 / 2000 / 32 / 8  49 : 51
+//             4 / 8000 / 256 / 4   37 : 43    16 / 4000 / 256 / 4  72 : 49    64 / 2000 / 64 / 8  88 : 59
+//   d = 128   1 / 16000 / 256 / 4  45 : 50    16 / 4000 / 64 / 8   50 : 52    64 / 2000 / 32 / 8  62 : 64
+//             4 / 8000 / 256 / 4   55 : 55    16 / 4000 / 256 / 4  90 : 61    64 / 2000 / 64 / 8  114 : 76
+//   d = 256   1 / 16000 / 128 / 4  65 : 68    16 / 4000 / 128 / 4  105 : 93   64 / 2000 / 64 / 8  263 : 306
+//             4 / 8000 / 256 / 4   83 : 80    16 / 4000 / 256 / 4  193 : 119  64 / 500 / 64 / 8   129 : 92
 void plan_tree(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
-    plan_attn(s, p, out);
-    if (out->variant != FC_ATTN_TILE) {
+    const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv), per = rows > 16 ? 32 : 16;
+    const int64_t base = (int64_t)(s->batch > 0 ? s->batch : 1) * s->hkv * ((rows + per - 1) / per);
+    const int64_t cus = fc::device_cu_count(), blocks = key_blocks(s, p, per);
+    fc_attn_params q = *p;
+    if (q.variant == FC_ATTN_AUTO) {
+        const bool few = rows <= (s->d > 128 ? 64 : 32) || (base <= cus && blocks * 16 <= (1 << 20) / base);
+        q.variant = few ? FC_ATTN_ROWS : FC_ATTN_TILE;
+    }
+    plan_attn(s, &q, out);
+    if (q.variant == FC_ATTN_ROWS) {
         // A split costs the join's launch and a second pass, 5 to 6 us: it has three steps of 256 keys at
         // least, and no block waits for a CU (us, by splits; trees of 8, 32 / 8 heads of 128):
         //   8 over 1000 keys     1: 12.8   2: 15.2   4: 17.8      1 over 513     1: 9.9   2: 13.1   4: 13.1
         //   2 over 2000          1: 17.5   2: 16.1   3: 15.4      8 over 4096    1: 31.4  2: 26.0   4: 27.4
         //   1 over 32768         4: 62     8: 43     16: 30       16 over 2000   1: 21.4  2: 26.5   4: 33
         if (p->splits > 0) return;
-        const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv), per = rows > 16 ? 32 : 16;
-        const int64_t base = (int64_t)(s->batch > 0 ? s->batch : 1) * s->hkv * ((rows + per - 1) / per);
-        const int64_t cus = fc::device_cu_count(), room = (rows > 16 && s->d > 64 ? cus / 2 : cus) / base;
-        const int64_t steps = (key_blocks(s, p, per) + 15) / 16, n = room < steps / 3 ? room : steps / 3;
-        fc_attn_params q = *p;
-        q.variant = FC_ATTN_ROWS;
+        const int64_t room = (rows > 16 && s->d > 64 ? cus / 2 : cus) / base;
+        const int64_t steps = (blocks + 15) / 16, n = room < steps / 3 ? room : steps / 3;
         q.splits = (int32_t)(n < 1 ? 1 : n);
         plan_attn(s, &q, out);
         return;
     }
     const TreeTiles t = tree_tiles(s, p);
-    const int64_t batch = s->batch > 0 ? s->batch : 1, per = t.even ? (t.even + batch - 1) / batch : 1;
-    out->splits = (int32_t)per;
-    out->chunk = (int32_t)((key_blocks(s, p, 0x7fffffff) + per - 1) / per * 16);
+    const int64_t batch = s->batch > 0 ? s->batch : 1, parts = t.even ? (t.even + batch - 1) / batch : 1;
+    out->splits = (int32_t)parts;
+    out->chunk = (int32_t)((key_blocks(s, p, 0x7fffffff) + parts - 1) / parts * 16);
     out->workspace = t.even ? t.slots * t.row_tiles * t.rows * s->hkv * (s->d + 4) * 4 + s->batch * 8 : 0;
 }
 
