@@ -237,7 +237,9 @@ TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
         t.even = t.even < stages / 8 ? t.even : stages / 8;
         if (s->batch * heads >= 4 * room || t.even <= 1) t.even = 0;
     }
-    if (s->batch > 4096 || p->splits == 1 || t.even * t.row_tiles > 0x7fffffff / 256 || heads > 65535) t.even = 0;
+    if (s->batch > 4096 || p->splits == 1 || heads > 65535) t.even = 0;
+    const int64_t most = 65535 / t.row_tiles;   // (a grid's)
+    t.even = t.even < most ? t.even : most > 1 ? most : 0;
     t.slots = t.even ? t.even + s->batch : 0;
     return t;
 }

@@ -264,7 +264,7 @@ def test_wide_heads_split(fc, variant, d, splits):
     check_tree(fc, b, bits, pos, "wide", max_q=60, variant=variant, splits=splits)
 
 
-@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("splits", [0, 1, 2, 1024])
 def test_many_sequences_some_empty(fc, splits):
     """More sequences than a wave has lanes, some without tokens or without new ones."""
     print("case many", splits, flush=True)
