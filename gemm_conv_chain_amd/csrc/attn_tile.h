@@ -70,11 +70,12 @@ __device__ __forceinline__ long alike(long v)
 // the keys of each in as many parts, the longest sequence's blocks end last.  So the
 // stages of all sequences are dealt out evenly to as many blocks as the machine
 // holds at once (AttnArgs::even); the tiles of a sequence go through the same keys
-// side by side, so that these are read from memory once.  Measured: 32 trees of 26
-// nodes over up to 8192 keys, 32 / 8 heads of 128, 107 us and 15 for the join (with a block a tile and
-// as many splits of every sequence as before, 159 in all), 364 MB of keys and 93 GFLOP of
-// 128 rows, 104 of which are nodes'; 2 of 60 over 100001, 226 to 244 and 14, 209 GFLOP at 0.86 to
-// 0.93 TFLOP/us: the two pipes together, as for prompts.
+// side by side, so that these are read from memory once.  Measured: 32 trees of up to
+// 26 nodes over up to 8192 keys, 32 / 8 heads of 128, 107 to 115 us and 15 for the join (with a block a
+// tile and as many splits of every sequence 159 in all): 364 MB of keys and 66 GFLOP, since small
+// trees leave waves of a tile idle, and a stage's steps, not a pipe, then take the time (matrix
+// pipe busy 0.25, waves wait 0.43 of their cycles).  2 of 60 over 100001, 226 to 244 and 14: 197
+// GFLOP at 0.81 to 0.87 TFLOP/us, the two pipes together, as for prompts.
 template <class T, int D, int NW, int MODE, bool TREE>
 __global__ __launch_bounds__(64 * NW, 2) void k_attn_tile(AttnArgs a, int row_tiles)
 {
