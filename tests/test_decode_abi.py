@@ -217,3 +217,21 @@ def test_binding_refusals_of_sampling():
         fc.sample_tokens(x, u, out=torch.zeros(2, dtype=torch.int64))
     with pytest.raises(TypeError, match="device"):
         fc.sample_tokens(x, u)
+
+
+def test_plans_of_trees():
+    """Few rows take the rows form and whole keys, a batch of wide trees the tile form; what is asked for is kept."""
+    few = fc.attn_plan(8, 1, 8, 2, 64, 16, 40, 8, 513, tree=True)
+    assert few["variant"] == "rows" and few["splits"] == 1 and few["workspace"] == 0
+    long = fc.attn_plan(8, 1, 32, 8, 128, 64, 512, 8, 32768, tree=True)
+    assert long["variant"] == "rows" and long["splits"] > 1 and long["workspace"] > 0
+    wide = fc.attn_plan(64 * 32, 64, 32, 4, 128, 64, 64, 32, 4000, tree=True)
+    assert wide["variant"] == "tile"
+    for variant in ("rows", "tile"):
+        one = fc.attn_plan(64, 4, 8, 2, 128, 64, 64, 16, 4000, variant=variant, splits=1, tree=True)
+        many = fc.attn_plan(64, 4, 8, 2, 128, 64, 64, 16, 4000, variant=variant, splits=7, tree=True)
+        assert one["variant"] == many["variant"] == variant
+        assert one["workspace"] == 0 and many["workspace"] > 0 and many["splits"] == 7
+    # blocks stay within a grid, whatever is asked for
+    huge = fc.attn_plan(4096, 4096, 8, 2, 64, 16, 64, 1, 1000, variant="tile", splits=1024, tree=True)
+    assert huge["splits"] <= 65535

@@ -252,6 +252,8 @@ def test_a_bound_that_is_too_small_costs_time_only(fc, variant, splits):
     lens, new = [300, 200, 129], [129, 40, 1]
     b, bits, pos = tree_batch(23, BF16, lens, new, 8, 2, 64, 32)
     check_tree(fc, b, bits, pos, "max_q", max_q=2, max_kv=300, variant=variant, splits=splits)
+    check_tree(fc, b, bits, pos, "max_kv", max_q=129, max_kv=20, variant=variant, splits=splits)
+    check_tree(fc, b, bits, pos, "both", max_q=1, max_kv=1, variant=variant, splits=splits)
 
 
 @pytest.mark.parametrize("variant", ["rows", "tile"])

@@ -291,3 +291,23 @@ def test_split_results_with_poisoned_lds(fc):
             with fc.poison_build():
                 p = fc.chain_attn(**g, tree=tree, max_q=33, variant=variant, splits=splits)
             assert torch.equal(a, p), (variant, splits)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_drawn_mixtures(fc, seed):
+    rng = random.Random(1000 + seed)
+    d, page, hkv, G = rng.choice([64, 128, 192, 256]), rng.choice([16, 32, 64, 128]), rng.choice([1, 2, 3]), rng.choice([1, 2, 4, 5])
+    new = [rng.choice([0, 1, 2, 7, 16, 31, 65]) for _ in range(rng.randint(1, 5))]
+    if not any(new):
+        new[0] = 3
+    lens = [n + rng.choice([0, 1, 15, 16, 100, 400]) for n in new]
+    kw = dict(max_q=rng.choice([max(new), max(new) + 9]), variant=rng.choice(["rows", "tile", "auto"]), splits=rng.choice([0, 0, 1, 2, 5]))
+    if rng.random() < 0.4:
+        kw["window"] = rng.choice([1, 5, 33, 200])
+    if rng.random() < 0.3:
+        kw["softcap"] = rng.choice([5.0, 30.0, 1000.0])
+    if rng.random() < 0.3:
+        kw["slopes"] = torch.tensor([rng.choice([0.0, 0.01, 0.5]) for _ in range(hkv * G)])
+    print("case drawn tree", seed, d, page, hkv, G, new, lens, kw, flush=True)
+    b, bits, pos = tree_batch(seed, rng.choice(DTYPES), lens, new, hkv * G, hkv, d, page, rng.choice([1, 6, 70]))
+    check(fc, b, bits, pos, "drawn %d" % seed, **kw)
