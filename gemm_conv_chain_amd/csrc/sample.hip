@@ -850,18 +850,20 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         return index_at(goal_of(u, block_sum(w)), n, left);
     }
 
+    // Logits of a cut row that are wanted at least, as far as top_k or top_p says.
+    __device__ __forceinline__ int wanted() const { return set.k > 0 ? set.k : set.p < 1.0f ? SR_NUCLEUS : 0x7fffffff; }
+
     // The elements in question of a cut row, if there are at most SR_LIST: into s.list; their number,
     // or -1.  *floored: those of less than the least weight are not among them.
     template <int SEGS, class G> __device__ __forceinline__ int gather(G groups, int ngroups, bool again, bool* floored)
     {
         *floored = false;
-        const bool mass = set.p < 1.0f && set.k == 0;
-        const unsigned first = set.k > 0 ? set.k : mass ? SR_NUCLEUS : 0x7fffffff;   // logits that are wanted at least
         if (set.k > SR_LIST) return -1;
+        const int first = wanted();
         // The least logit in question: so many groups hold one each down to a bin, or (the second time)
         // down to a value.
         float floor = kNegInf;
-        if (first <= (unsigned)ngroups) {
+        if (first <= ngroups) {
             const Tops<G> source{*this, groups, ngroups};
             if (again) {
                 if (cut_at<false>(source, source, first, 0.0f, [](u64, float) { return 0; }, nullptr)) floor = s.cut_x;
@@ -891,7 +893,10 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         }
         __syncthreads();
         const int nc = s.n_chosen;
-        if (nc > SR_LIST) return -1;   // (each holds one at least)
+        if (nc > SR_LIST) {            // (each holds one at least)
+            __syncthreads();           // every wave has read the count, which a second call resets
+            return -1;
+        }
         for (int e = tid; e < nc * SEGS; e += THREADS) {
             const int g = s.chosen[e / SEGS];
             // group g of 32: lane g % 64 of batch g / 64; of 8: lane g % 64 of a batch's quarter g / 64
@@ -908,7 +913,10 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         }
         __syncthreads();
         const int n = s.n_list;
-        if (n > SR_LIST) return -1;
+        if (n > SR_LIST) {
+            __syncthreads();           // (as above)
+            return -1;
+        }
         if (tid < n) {
             const Entry e = s.list[tid];
             s.list[tid] = entry(__builtin_bit_cast(float, (unsigned)e[0]), e[1], weight(__builtin_bit_cast(float, (unsigned)e[0])));
@@ -959,9 +967,11 @@ template <class L, int WAVES, bool ROW> struct Sampler {
                 all = block_sum(all);
             }
             bool floored;
+            const int ngroups = a.batches * (SEGS == 4 ? 64 : 256);
+            const int times = wanted() <= ngroups ? 2 : 1;   // (where the groups say nothing, a second look finds the same)
             int n = -1;
 #pragma unroll 1
-            for (int again = 0; again < 2 && n < 0; ++again) n = gather<SEGS>(groups, a.batches * (SEGS == 4 ? 64 : 256), again, &floored);
+            for (int again = 0; again < times && n < 0; ++again) n = gather<SEGS>(groups, ngroups, again, &floored);
             return n < 0 ? SR_NOT_YET : draw_short(n, floored, all, u);
         }
         // the batch that u lies in: thread t has `per` batches
