@@ -1209,7 +1209,8 @@ def tree_accept(parents, drafted, targets, cu_q, kv_lens, max_q=None):
     """(keep [batch, max_q], kept [batch], next [batch], lens [batch]), all int32: each tree
     walked from node 0, the token that the last step decided, to the first child whose
     ``drafted`` token is the one that ``targets`` holds for the present node (the model's own
-    choice there, of ``sample_tokens``), until there is none.  ``keep``: the nodes passed, rising,
+    choice there, of ``sample_tokens``), until there is none or that target is under 0 (its mark
+    of a row it cannot draw from).  ``keep``: the nodes passed, rising,
     -1 behind them; ``kept``: how many; ``next``: the target of the last; ``lens``: the
     sequence's length with them."""
     T, = _ndim(parents, "parents", 1)

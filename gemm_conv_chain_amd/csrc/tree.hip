@@ -75,7 +75,8 @@ __global__ __launch_bounds__(256) void k_tree_plan(const int* parents, const int
 }
 
 // One wave a sequence.  A child comes after its parent, so that one pass over the nodes, 64
-// at a time in registers, meets the whole path.
+// at a time in registers, meets the whole path.  A target under 0 is no token (what sample_tokens
+// gives for a row that is no distribution): no draft is it, and the path ends there.
 __global__ __launch_bounds__(256) void k_tree_accept(const int* parents, const int* drafted, const int* targets, const int* cu_q,
                                                      const int* kv_lens, KvShape s, int max_keep, int* keep, int* kept, int* next,
                                                      int* lens)
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(256) void k_tree_accept(const int* parents, const i
                 count = 1;
                 want = __builtin_amdgcn_readfirstlane(tgt);
             }
-            while (count < max_keep) {
+            while (count < max_keep && want >= 0) {
                 const unsigned long long m = __ballot(live && par == cur && j > cur && tok == want);
                 if (!m) break;
                 const int at = __builtin_ctzll(m);

@@ -672,7 +672,9 @@ fc_status chain_attn_tree(const void *q, const int64_t *strides, const uint8_t *
 /*
  * tree_accept -- walks each tree along the model's own choices: from node 0 on
  * to the first child whose drafted token [tokens] is the token that targets
- * [tokens] holds for the present node, until there is none.  keep
+ * [tokens] holds for the present node, until there is none.  A target under 0
+ * (sample_tokens' mark of a row that it cannot draw from) is nobody's token: the
+ * path ends there and next is that target.  keep
  * [batch][max_keep]: the nodes passed, rising, then -1 (a path longer than
  * max_keep ends there); kept [batch] their number; next [batch] = targets of the
  * last one, the step's new token; lens [batch] = kv_lens - n + kept.  A sequence
