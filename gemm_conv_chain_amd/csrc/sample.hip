@@ -21,7 +21,8 @@
 // integer sums do not depend on their order, and with it the token.  32-bit
 // weights would be off by 1e-7 of the mass, a token in as many million rows.
 // A batch's sum, whose unit its own largest is, is brought to the row's by one
-// product in 64 bits, rounded down.
+// product in 64 bits, rounded down; the row's mass is the sum of these in every
+// kernel, so that a row's token does not depend on which of them draw it.
 //
 // Bound by the vector unit where many rows need their sums (some 25
 // instructions of 64 bits a logit; 128 x 131072 in bf16: 17 us for the pass,
@@ -45,7 +46,19 @@ constexpr int SR_LONG = 16;        // and from all of a row
 constexpr int SR_LIST = 64 * SR_SHORT;   // elements in question that a row's largest may be
 constexpr int SR_NUCLEUS = 256;    // logits that a cut by mass alone looks at first
 constexpr double SR_ONE = 0x1p42;  // a weight of 1
-constexpr int SR_NOT_YET = -2;     // in out: the row is k_sample_long's
+// In out: the row is k_sample_long's. Such a mark also says how large the row's mass is by its batches'
+// sums, which a share of the mass (top_p) is taken of whichever kernels draw the row: SR_NOT_YET less
+// that mass's low 30 bits. k_sample_long sums the weights in the row's units, and the two differ by far
+// less than 2^29: by half a unit or less a weight on either side (2^20 in all), a unit a batch, and the
+// 64-bit rounding of exponentials and products, under 2^-44 of at most 2^62.
+constexpr int SR_NOT_YET = -2;
+constexpr unsigned SR_MARK = (1u << 30) - 1;
+__device__ __forceinline__ int not_yet(u64 mass) { return SR_NOT_YET - (int)((unsigned)mass & SR_MARK); }
+__device__ __forceinline__ u64 marked_mass(int mark, u64 near)
+{
+    const unsigned low = (unsigned)(SR_NOT_YET - mark);
+    return near + (long long)((int)((low - (unsigned)near) << 2) >> 2);
+}
 
 struct SampleArgs {
     const void* logits;
@@ -341,6 +354,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     RowSet set;
     double max;
     float max_x, unit;      // bins of the histogram a unit of x
+    int mark;               // (ROW: what out held)
 
     __device__ __forceinline__ u64 weight(float x) const { return weight_of(x, max, set.slope, set.far, s.table); }
     __device__ __forceinline__ int bin(float x) const { return (int)fminf((max_x - x) * unit, (float)(BINS - 1)); }
@@ -635,7 +649,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     }
 
     // The last element that stays, in s.cut_x and s.cut_i: the goal-th in falling order, or (MASS)
-    // that at which the mass reaches goal; `share` > 0: that share of the whole mass.  False where there are not so many.  `tie(many, x)`: the
+    // that at which the mass reaches goal; `share` > 0: that share of the marked mass.  False where there are not so many.  `tie(many, x)`: the
     // index of the many-th element that is x.  Of a row, *mine: the sum of this wave's part in the bins
     // before the cut's, whose largest value may be s.cut_top; or (cut_top -inf) with what stays of that.
     // `look`: the source, for passes that do little.
@@ -648,7 +662,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             u64 v = 0;
 #pragma unroll
             for (int k = 0; k < WAVES; ++k) v += s.bins[ROW ? k : 0][tid];
-            goal = (u64)__builtin_ceil((double)share * (double)block_sum(v));
+            goal = (u64)__builtin_ceil((double)share * (double)marked_mass(mark, block_sum(v)));
         }
         u64 ahead;
         const int b = find_bin(goal, &ahead);
@@ -815,7 +829,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
         });
     }
 
-    // The same from the n elements of s.list. SR_NOT_YET: their mass is too little (floored: what they
+    // The same from the n elements of s.list. not_yet: their mass is too little (floored: what they
     // lack would not stay).
     __device__ __forceinline__ int draw_short(int n, bool floored, u64 all, float u)
     {
@@ -841,7 +855,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
                 cut_x = s.cut_x;
                 cut_i = s.cut_i;
             } else if (!floored) {
-                return SR_NOT_YET;
+                return not_yet(all);
             }
             __syncthreads();
         }
@@ -972,7 +986,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
             int n = -1;
 #pragma unroll 1
             for (int again = 0; again < times && n < 0; ++again) n = gather<SEGS>(groups, ngroups, again, &floored);
-            return n < 0 ? SR_NOT_YET : draw_short(n, floored, all, u);
+            return n < 0 ? not_yet(all) : draw_short(n, floored, all, u);
         }
         // the batch that u lies in: thread t has `per` batches
         const int per = (a.batches + THREADS - 1) / THREADS;
@@ -1026,7 +1040,7 @@ __global__ __launch_bounds__(64 * SR_SHORT) void k_sample(SampleArgs a)
     fill_table(s.table, threadIdx.x);
     __syncthreads();
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        Sampler<L, SR_SHORT, false> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f};
+        Sampler<L, SR_SHORT, false> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f, 0};
         for (int b = wave; b < a.batches; b += SR_SHORT) {
             const BatchInfo info = scan_batch<1>(w.row, b * SR_BATCH, a.vocab, lane, w.set, groups + b * 256, s.table);
             if (lane == 0) infos[b] = info;
@@ -1067,7 +1081,7 @@ __global__ __launch_bounds__(64 * SR_SHORT) void k_sample_pick(SampleArgs a)
     fill_table(s.table, threadIdx.x);
     __syncthreads();
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        Sampler<L, SR_SHORT, false> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f};
+        Sampler<L, SR_SHORT, false> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f, 0};
         const int token = w.template draw<4>(r, (const BatchInfo*)a.info + r * a.batches, (const float*)a.groups + r * a.batches * 64);
         if (threadIdx.x == 0) a.out[r] = token;
         __syncthreads();
@@ -1083,10 +1097,11 @@ __global__ __launch_bounds__(64 * SR_LONG) void k_sample_long(SampleArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     bool filled = false;
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
-        if (a.out[r] != SR_NOT_YET) continue;
+        const int mark = __builtin_amdgcn_readfirstlane(a.out[r]);
+        if (mark > SR_NOT_YET) continue;
         if (!filled) fill_table(s.table, threadIdx.x);
         filled = true;
-        Sampler<L, SR_LONG, true> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f};
+        Sampler<L, SR_LONG, true> w{a, s, (const L*)a.logits + r * a.stride, lane, wave, (int)threadIdx.x, row_set(a, r), 0.0, 0.0f, 0.0f, mark};
         float top = kNegInf;
         if (a.info) {
             const BatchInfo* const infos = (const BatchInfo*)a.info + r * a.batches;
