@@ -233,10 +233,10 @@ TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
     const int64_t heads = t.row_tiles * s->hkv;
     const int64_t stages = s->batch * (key_blocks(s, p, 0x7fffffff) * 16 / keys + 1);
     t.even = p->splits > 0 ? (int64_t)p->splits * s->batch : (room + heads / 2) / heads;
-    if (p->splits == 0) {
-        t.even = t.even < stages / 8 ? t.even : stages / 8;
-        if (s->batch * heads >= 4 * room || t.even <= 1) t.even = 0;
-    }
+    // (more parts than stages are not worked on: they would be workspace and blocks for nothing)
+    const int64_t parts = p->splits > 0 ? stages : stages / 8;
+    t.even = t.even < parts ? t.even : parts;
+    if (t.even <= 1 || (p->splits == 0 && s->batch * heads >= 4 * room)) t.even = 0;
     if (s->batch > 4096 || p->splits == 1 || heads > 65535) t.even = 0;
     const int64_t most = 65535 / t.row_tiles;   // (a grid's)
     t.even = t.even < most ? t.even : most > 1 ? most : 0;

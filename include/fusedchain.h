@@ -659,9 +659,10 @@ fc_status tree_plan(const int32_t *parents, const int32_t *cu_q, const int32_t *
  * nodes of its bits; slopes and windows take the distance of positions, a slot
  * before the tree being its own.  params->causal has to be set, the other
  * arguments are chain_attn's.  Of its forms TILE shares the work of all trees
- * evenly among its blocks; params->splits then is how many of these there are for
- * a tile of 128 rows (256 for d > 128).  The workspace's size is
- * chain_attn_tree_plan's.
+ * evenly among its blocks; params->splits times the batch then is how many of these
+ * there are for a tile of 128 rows (256 for d > 128), or as many as there are
+ * stages of 64 keys (32 for d = 256) by max_kv, if that is less.  The workspace's
+ * size is chain_attn_tree_plan's.
  */
 fc_status chain_attn_tree_plan(const fc_kv_shape *shape, const fc_attn_params *params, fc_attn_plan *plan);
 fc_status chain_attn_tree(const void *q, const int64_t *strides, const uint8_t *codes, const float *scales,
