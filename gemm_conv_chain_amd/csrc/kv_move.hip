@@ -68,6 +68,13 @@ __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
     Source* const sources = reinterpret_cast<Source*>(lds + sizeof(KeepShared));
     uint8_t* const sk = lds + sizeof(KeepShared) + sizeof(Source) * a.staged;
     uint8_t* const sv = sk + a.staged * D;
+    const auto poison = [&](void* from) {   // (poison build) all from there on
+        if constexpr (kPoison) {
+            lds_poison(from, (int)(sv + a.staged * D - (uint8_t*)from), tid, 256);
+            __syncthreads();
+        }
+    };
+    poison(lds);
     if (tid == 0) sh.bad = sh.moves = 0;
     __syncthreads();
     bool bad = false, moves = false;
@@ -196,6 +203,7 @@ __global__ __launch_bounds__(256) void k_kv_keep(KeepArgs a)
         }
         if (tid < 2 * pages && sh.id[tid >> 1] >= 0) *scale_at(sh.id[tid >> 1], tid & 1) = now(tid >> 1, tid & 1);
         __syncthreads();   // LDS is free again
+        poison(lds);
         p += pages;
         i0 += cnt;
     }

@@ -497,6 +497,7 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     template <bool ALL = true> __device__ __forceinline__ int find_bin(u64 goal, u64* before)
     {
         __syncthreads();
+        if constexpr (kPoison) lds_poison(s.few, sizeof(s.few), tid, THREADS);   // free from here on
         if (tid == 0) {
             s.n_few = 0;
             s.key_lo = ~0u;
@@ -873,6 +874,12 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     {
         *floored = false;
         if (set.k > SR_LIST) return -1;
+        if constexpr (kPoison) {   // all of a call before is done with these
+            lds_poison(s.list, sizeof(s.list), tid, THREADS);
+            lds_poison(s.chosen, sizeof(s.chosen), tid, THREADS);
+            if (tid == 0) s.n_list = s.n_chosen = kPoisonWord;
+            __syncthreads();
+        }
         const int first = wanted();
         // The least logit in question: so many groups hold one each down to a bin, or (the second time)
         // down to a value.
@@ -1028,6 +1035,16 @@ template <class L, int WAVES, bool ROW> struct Sampler {
     __device__ __forceinline__ u64 joined(BatchInfo b) const { return (u64)((double)high_pair(b) * scale_of(b)); }
 };
 
+// Poison build: all that the block has, and `more` bytes behind it.
+template <int WAVES, bool ROW>
+__device__ __forceinline__ void poison_shared(FC_LDS Shared<WAVES, ROW>& s, int more, int tid)
+{
+    if constexpr (kPoison) {
+        lds_poison(&s, sizeof s + more, tid, 64 * WAVES);
+        __syncthreads();
+    }
+}
+
 // One block a row: the infos and groups stay in LDS (vocabularies to 32768).
 template <class L>
 __global__ __launch_bounds__(64 * SR_SHORT) void k_sample(SampleArgs a)
@@ -1037,6 +1054,7 @@ __global__ __launch_bounds__(64 * SR_SHORT) void k_sample(SampleArgs a)
     FC_LDS BatchInfo* const infos = (FC_LDS BatchInfo*)(&s + 1);
     FC_LDS float* const groups = (FC_LDS float*)(infos + a.batches);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    poison_shared(s, a.batches * (sizeof(BatchInfo) + 1024), threadIdx.x);
     fill_table(s.table, threadIdx.x);
     __syncthreads();
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -1078,6 +1096,7 @@ __global__ __launch_bounds__(64 * SR_SHORT) void k_sample_pick(SampleArgs a)
     extern __shared__ __align__(16) uint8_t raw[];
     FC_LDS Shared<SR_SHORT, false>& s = *(FC_LDS Shared<SR_SHORT, false>*)raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    poison_shared(s, 0, threadIdx.x);
     fill_table(s.table, threadIdx.x);
     __syncthreads();
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
@@ -1096,6 +1115,7 @@ __global__ __launch_bounds__(64 * SR_LONG) void k_sample_long(SampleArgs a)
     FC_LDS Shared<SR_LONG, true>& s = *(FC_LDS Shared<SR_LONG, true>*)raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     bool filled = false;
+    poison_shared(s, 0, threadIdx.x);
     for (long r = blockIdx.x; r < a.rows; r += gridDim.x) {
         const int mark = __builtin_amdgcn_readfirstlane(a.out[r]);
         if (mark > SR_NOT_YET) continue;

@@ -23,6 +23,11 @@ __global__ __launch_bounds__(256) void k_tree_plan(const int* parents, const int
     __shared__ int out[TREE_NODES];                    // the first ancestor before them, or -1
     const int lane = threadIdx.x & 63;
     for (int b = blockIdx.x; b < s.batch; b += gridDim.x) {
+        if constexpr (kPoison) {
+            lds_poison(among, sizeof among, threadIdx.x, blockDim.x);
+            lds_poison(out, sizeof out, threadIdx.x, blockDim.x);
+            __syncthreads();
+        }
         long tok0;
         int n;
         seq_range(cu_q, s, b, &tok0, &n);
