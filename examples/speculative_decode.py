@@ -10,7 +10,8 @@ on the embedding alone.  One step, for every sequence at once:
     its keys and values move to the front of the tree's slots            kv_keep
 
 Every step adds 1 to DEPTH + 1 tokens to a sequence, drawn as the model alone would
-draw them.  Two sequences continue each prompt: the second shares its pages, but for
+draw them, up to roundings (a rejected draft may have raised the scale of a page, by
+which small codes of other tokens on it were rounded once more).  Two sequences continue each prompt: the second shares its pages, but for
 the last, partly filled one, which is copied (KvPages, kv_copy).  The step is captured
 in a HIP graph and replayed; the host reads the tokens behind it.
 

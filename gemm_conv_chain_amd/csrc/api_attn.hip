@@ -253,6 +253,8 @@ TreeTiles tree_tiles(const fc_kv_shape* s, const fc_attn_params* p)
 //             4 / 8000 / 256 / 4   55 : 55    16 / 4000 / 256 / 4  90 : 61    64 / 2000 / 64 / 8  114 : 76
 //   d = 256   1 / 16000 / 128 / 4  65 : 68    16 / 4000 / 128 / 4  105 : 93   64 / 2000 / 64 / 8  263 : 306
 //             4 / 8000 / 256 / 4   83 : 80    16 / 4000 / 256 / 4  193 : 119  64 / 500 / 64 / 8   129 : 92
+// The rule takes the slower one for some of these heads of 256: 64 / 500 / 64 / 8 and 16 / 4000 / 128 / 4
+// go by rows, for which more keys (64 / 2000) and fewer sequences (1 / 16000) speak.
 void plan_tree(const fc_kv_shape* s, const fc_attn_params* p, fc_attn_plan* out)
 {
     const int64_t rows = (int64_t)(s->max_q > 0 ? s->max_q : 1) * (s->hq / s->hkv), per = rows > 16 ? 32 : 16;

@@ -1200,9 +1200,10 @@ __global__ __launch_bounds__(64) void k_sample_tiny(SampleArgs a)
 }
 
 // Whether one block takes in a row at once, rather than the pass over the logits by many and the
-// rest by one.  Two launches less, but a row's exponentials all on one CU, and rows past two a CU
+// rest by one.  One launch less, but a row's exponentials all on one CU, and rows past two a CU
 // wait for a second round of the whole.  Measured, at once against apart (us; the whole distribution,
-// top_k 50, top_p 0.95 with some flat rows):
+// top_k 50, top_p 0.95 with some flat rows; the rule is off by 2 us for the 128 x 17000 below, the most
+// that it was seen to lose without flat rows):
 //      1 x 9000   10.3 14 18  against 11 16 20        1 x 32000   14.3 17 23  against 12.4 18 21
 //   128 x 17000   12.8 17 57  against 14.7 19 55    128 x 32000   15.5 18 71  against 15.2 20 58
 //   600 x 9000    29   49 79  against 25   43 100   600 x 32000   41.5 63 115 against 36   48 92

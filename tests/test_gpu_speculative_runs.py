@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 # to fp16 by 2^-7 at most in either run: 2^-6.  Six roundings before that (q, attention's result, its
 # product, h, the hidden layer, y), each of 2^-11 / sqrt(3) of 1.2 rms, go through matrices of gain one and
 # then the head: 4 * sqrt(6) * 3.4e-4 = 3.3e-3 rms, times sqrt(2) for two runs, times 6 deviations: 0.028.
-# Scales that rejected drafts raised move codes by 2^-10 of a page's scale, 2^-18 of its largest value: nothing
+# Scales that rejected drafts raised move codes by 2^-9 of a page's scale, 2^-16 of its largest value: nothing
 # beside these.  A greedy choice compares two logits, each off by 0.016 + 0.028.
 NEAR = 0.1
 
